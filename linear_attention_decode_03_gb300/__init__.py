@@ -16,6 +16,11 @@ weights prepared once, then ``run(projected, out, caches=..., slots=...,
 accepted=None)`` per step, with ``accepted[:R]`` and contiguous ``slots[:R]``
 for verify steps; ``plan(...)`` records a step with fixed buffers as a CUDA
 graph (:class:`KdaPlan`) that each later step launches in one call.
+
+The operators around the core (``include/kda_ops.h``, module ``ops``) are
+functions of tensors: :func:`quant_rows` and :func:`linear_i8` (the projections
+on 8-bit operands), :func:`la_step` and :func:`la_prefill` (linear attention with
+a decay a head), with :func:`kda_linear_i8_check` and :func:`kda_la_check`.
 """
 from __future__ import annotations
 
@@ -30,12 +35,16 @@ __all__ = [
     "kda_strerror", "kda_launch_info", "kda_set_gate_mode", "kda_plan_create", "kda_layer_plan_create", "kda_plan_launch",
     "kda_plan_destroy", "kda_set_state_dtype", "kda_set_v_split", "kda_linear", "kda_linear_check", "linear", "PreparedKda", "KdaPlan", "KDA_STATE_F32", "KDA_STATE_BF16", "KDA_PDL_STEP", "KDA_PDL_O_PROJ", "KDA_ERR_SLOT", "KDA_ERR_ACCEPTED",
     "KDA_ERR_TIMEOUT", "KDA_ERR_DUPLICATE", "KDA_MAX_TOKENS", "DEBUG_LIB_PATH", "KDA_GATE_SIGMOID", "KDA_GATE_SOFTPLUS", "HEAD_DIM",
+    "quant_rows", "linear_i8", "la_step", "la_prefill", "la_prefill_workspace", "kda_linear_i8_check", "kda_la_check",
+    "KDA_ERR_SEQ", "KDA_QUANT_MAX_COLS",
 ]
 
 HEAD_DIM = 128
 KDA_OK, KDA_EINVAL, KDA_ECUDA = 0, -1, -2
 KDA_ERR_SLOT, KDA_ERR_ACCEPTED, KDA_ERR_TIMEOUT, KDA_ERR_DUPLICATE = 1, 2, 4, 8
+KDA_ERR_SEQ = 16
 KDA_MAX_TOKENS = 8
+KDA_QUANT_MAX_COLS = 32768
 KDA_GATE_SIGMOID, KDA_GATE_SOFTPLUS = 0, 1
 KDA_STATE_F32, KDA_STATE_BF16 = 0, 1
 KDA_PDL_STEP, KDA_PDL_O_PROJ = 1, 2
@@ -89,8 +98,42 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kda_linear.restype = i32
     lib.kda_linear_check.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
     lib.kda_linear_check.restype = i32
+    _declare_ops(lib)
     _lib = lib
     return lib
+
+
+def _declare_ops(lib) -> None:
+    """Argument types of the functions of kda_ops.h."""
+    vp, ll, i32, f32 = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_float
+    flags = ctypes.POINTER(ctypes.c_uint)
+    lib.kda_quant_rows.argtypes = [vp, ll, ll, ll, vp, ll, vp, f32, vp, ll, vp, vp]
+    lib.kda_linear_i8.argtypes = [vp, ll, ll, vp, vp, vp, ll, ll, vp, ll, vp]
+    lib.kda_linear_i8_check.argtypes = [vp, flags]
+    lib.kda_la_step.argtypes = [vp, ll, vp, ll, vp, ll, ll, i32, i32, vp, ll, f32, vp, i32, ll, vp, vp, ll, vp]
+    lib.kda_la_prefill.argtypes = [vp, ll, vp, ll, vp, ll, ll, i32, i32, vp, ll, f32, vp, ll, ll, vp, vp, i32, ll,
+                                   vp, vp, ll, vp, ll, vp]
+    lib.kda_la_prefill_workspace.argtypes = [ll, i32, ll, ll]
+    lib.kda_la_check.argtypes = [vp, flags]
+    for name in ("kda_quant_rows", "kda_linear_i8", "kda_linear_i8_check", "kda_la_step", "kda_la_prefill",
+                 "kda_la_check"):
+        getattr(lib, name).restype = i32
+    lib.kda_la_prefill_workspace.restype = ll
+
+
+_OPS = ("quant_rows", "linear_i8", "la_step", "la_prefill", "la_prefill_workspace", "kda_linear_i8_check",
+        "kda_la_check")
+
+
+def __getattr__(name):
+    # the tensor functions need torch when they are defined; this module imports without it
+    if name in _OPS:
+        from . import ops
+
+        for n in _OPS:
+            globals()[n] = getattr(ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def kda_strerror(code: int) -> str:
