@@ -14,7 +14,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("kda_step.cu", "kda_linear.cu", "kda_quant.cu",
                                                       "kda_linear_i8.cu", "kda_la.cu")]
-HEADERS = [os.path.join(ROOT, "include", f) for f in ("kda.h", "kda_ops.h")]
+HEADERS = [os.path.join(ROOT, "include", f) for f in ("kda.h", "kda_ops.h")] + [
+    os.path.join(PKG_DIR, "csrc", f) for f in ("internal.h", "tc.cuh")]
 LIB_PATH = os.path.join(PKG_DIR, "libkda.so")
 # KDA_DEBUG build: adds the device check for duplicate slots in a step (KDA_ERR_DUPLICATE)
 DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libkda_debug.so")

@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "kda_ops.h"
+#include "tc.cuh"
 
 namespace {
 
@@ -37,13 +38,6 @@ struct LaArgs {
   int heads, share;  // share: value heads a query / key head
   float scale;
 };
-
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
 
 // A warp's 16 v rows of a state: KL k values a lane, RL rows a lane.  fp32: lane l has
 // k = 4 l .. + 3 of every row (a row is one 512-byte access of the warp); bf16: the
@@ -177,51 +171,624 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
   if (!(lane & 1)) *o = __float2bfloat16_rn(a.scale * t);
 }
 
-// The prompt form token by token: a warp keeps its 16 v rows over the sequence.
-template <bool BF>
-__global__ void __launch_bounds__(32 * STEP_WARPS) la_scan_kernel(const LaArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long task = blockIdx.x / STEP_SPLIT;
-  const int v0 = (blockIdx.x % STEP_SPLIT) * STEP_ROWS + (threadIdx.x >> 5) * 16;
-  const long long i = task / a.heads;
-  const int h = (int)(task % a.heads), hk = h / a.share;
-  const long long begin = a.cu[i], end = a.cu[i + 1];
-  if (begin < 0 || end < begin || end > a.rows || end - begin > a.max_len) {
-    if (threadIdx.x == 0) atomicOr(&g_la_err, KDA_ERR_SEQ);
-    return;
-  }
-  const int slot = a.slots[i];
-  const bool pad = slot == -1;
-  if (!pad && (slot < 0 || slot >= a.pool)) {
-    if (threadIdx.x == 0) atomicOr(&g_la_err, KDA_ERR_SLOT);
-    return;
-  }
-  __nv_bfloat16* o = a.out + h * D + v0 + (lane >> 1);
-  if (pad) {
-    for (long long t = begin; t < end; ++t)
-      if (!(lane & 1)) o[t * a.ldo] = __float2bfloat16_rn(0.0f);
-    return;
-  }
-  void* st = state_at(a, BF, slot, h, v0);
-  Slice<BF> S;
-  if (a.has_state && a.has_state[i])
-    S.load(st, lane);
-  else
-    S.zero();
-  for (long long t = begin; t < end; ++t) {
-    float q[Slice<BF>::KL], k[Slice<BF>::KL];
-    uint32_t v[8];
-    Slice<BF>::load_k(q, a.q + t * a.ldq + hk * D, lane);
-    Slice<BF>::load_k(k, a.k + t * a.ldk + hk * D, lane);
-    load_v16(v, a.v + t * a.ldv + h * D + v0);
-    const float d = expf(a.g[t * a.ldg + h]);
-    const float r = S.update(d, v, k, q, lane);
-    if (!(lane & 1)) o[t * a.ldo] = __float2bfloat16_rn(a.scale * r);
-  }
-  S.store(st, lane);
+// ---------------------------------------------------------------------------
+// Prompts.  With G_i the sum of the log decays of tokens 0..i of a chunk (C = 128
+// tokens), R_j that of the tokens behind j, and S the state before the chunk,
+//   o_i = scale (e^{G_i} S q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
+//   S'  = e^{G_C} S + sum_j v_j (e^{R_j} k_j)^T
+// so a chunk is matrix products: scores Q K^T, their decayed lower triangle P times V, Q S^T, and
+// V^T K' with K' the decayed keys.  One CTA takes a segment (a run of chunks of one
+// sequence and head) and carries S from chunk to chunk in fp32 registers; the
+// products run on tcgen05 into four 128-column accumulators, the whole tensor
+// memory.  Every exponent is at most 0.
+//
+// What is rounded: P and, as an operand of Q S^T, S to bf16 (an output of bf16
+// anyway).  The state itself is summed from exact parts: K' = hi + mid + lo in bf16 (24
+// bits; hi + mid where the pool is bf16), smallest first, each chunk's sum added to S
+// in fp32 registers, so that nothing accumulates in the tensor pipe over chunks.
+//
+// Roles (warps): 0-7 compute, 8 TMA copies and the decays, 9 MMAs.  Per chunk
+//   MMA:      QK, QS          | V^T K'            | PV
+//   compute:  K -> K'  | scores -> P | S += V^T K', its bf16 | outputs
+// and the copies of the next chunk's Q, K and V go out as soon as this one's last reader is done.
+//
+// A long sequence is split into segments to fill the GPU: la_chunk_kernel<., true> computes
+// each segment's own contribution to the state, la_join_kernel turns these into the states the
+// segments start from, and la_chunk_kernel<., false> runs all segments at once.
+constexpr int CHUNK = 128;
+constexpr int BOX = 64 * 128 * 2;          // 64 columns of 128 rows, bf16
+constexpr int TILE = 2 * BOX;              // a 128 x 128 bf16 operand
+constexpr int COMPUTE = 256;               // threads of the compute warps
+constexpr int CHUNK_THREADS = COMPUTE + 64;
+constexpr int MISC = 2048;                 // ChunkMisc
+constexpr int CHUNK_SMEM = 7 * TILE + MISC + 1024;  // (1024: the alignment of the swizzled tiles)
+static_assert(CHUNK_SMEM <= 227 * 1024, "shared memory of one CTA");
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float G_MIN = -104.0f;  // e^-104 is below fp32's smallest step
+
+// segments of a sequence of `len` tokens: runs of m chunks; an empty one has one, without chunks
+__device__ __forceinline__ long long seg_count(long long len, int m) {
+  const long long per = (long long)m * CHUNK;
+  return len <= per ? 1 : (len + per - 1) / per;
+}
+__device__ __forceinline__ bool seq_ok(const LaArgs& a, long long begin, long long end) {
+  return begin >= 0 && end >= begin && end <= a.rows && end - begin <= a.max_len;
 }
 
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+// Sequences before `seq` have `first` segments together; found by one warp.
+struct Segment {
+  int seq, index, count;  // which sequence; which of its `count` segments
+  long long begin, end;   // the sequence's rows
+};
+// Segment number `want` of all (by_seq false) or the first segment of sequence `want`
+// (by_seq true), whose number goes to *number.  False if there is none, or if it is not
+// below `limit` with the rest of its sequence: ascending cu_seqlens never get there, and
+// overlapping ones stay within the grid and the workspace.
+__device__ bool find_segment(const LaArgs& a, int m, long long limit, long long want, bool by_seq, Segment* s, long long* number) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (long long i0 = 0; i0 < a.seqs; i0 += 32) {
+    const long long i = i0 + lane;
+    long long b = 0, e = 0;
+    int n = 0;
+    if (i < a.seqs) {
+      b = a.cu[i], e = a.cu[i + 1];
+      if (seq_ok(a, b, e)) n = (int)seg_count(e - b, m);
+    }
+    long long upto = n;  // segments of the sequences i0 .. i
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += t;
+    }
+    const bool here = by_seq ? i == want && n > 0 : n > 0 && before + upto - n <= want && want < before + upto;
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    if (who) {
+      const int l = __ffs(who) - 1;
+      const long long first = __shfl_sync(0xffffffffu, before + upto - n, l);
+      s->seq = (int)(i0 + l);
+      s->count = __shfl_sync(0xffffffffu, n, l);
+      s->begin = __shfl_sync(0xffffffffu, b, l);
+      s->end = __shfl_sync(0xffffffffu, e, l);
+      s->index = by_seq ? 0 : (int)(want - first);
+      *number = first + s->index;
+      return first + s->count <= limit;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+struct ChunkArgs {
+  LaArgs a;
+  float* ws;      // [segments, heads, 128 (v), 128 (k)]: a segment's own state, then the one it starts from
+  float* decays;  // [segments, heads]: log2 of the decay over a segment
+  int m;          // chunks a segment
+  long long segments;  // at most
+};
+
+enum {  // barriers: completed by copies and MMAs (one arrival), ...
+  FULL_Q, FULL_K, FULL_V, EMPTY_Q, EMPTY_V, SCORES, DELTA, OUT, DRAIN, DECAY,
+  EMPTY_K,                     // ... by the 8 compute warps (and QK's commit), ...
+  KP, P_IN, S_IN, O_READ,      // ... by the 8 compute warps, ...
+  PAIR, BARS = PAIR + 4        // ... by the two warps of a quarter of the rows
+};
+struct ChunkMisc {
+  float G[CHUNK];  // G_i (log2)
+  float W[CHUNK];  // e^{R_j}, used up to the sequence's end
+  float E[CHUNK];  // e^{G_b - G_j}, G_b the last G of j's block of 16
+  float total;     // G_C (log2)
+  int found, dead;
+  uint32_t tmem;
+  long long number;
+  Segment seg;
+  unsigned long long bars[BARS];
+};
+static_assert(sizeof(ChunkMisc) <= MISC, "misc area");
+
+template <bool BF, bool LOCAL>
+__global__ void __launch_bounds__(CHUNK_THREADS, 1)
+    la_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv, const ChunkArgs p) {
+  const LaArgs& a = p.a;
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  // (all shared memory is dynamic: the seven operand tiles leave no room for a second alignment)
+  const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
+  const uint32_t sq = base, sk = base + TILE, sv = base + 2 * TILE, skp = base + 3 * TILE, ss = base + 6 * TILE;
+  ChunkMisc& sm = *reinterpret_cast<ChunkMisc*>(dyn + (base - smem_addr(dyn)) + 7 * TILE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (int)(blockIdx.x % a.heads), hk = h / a.share;
+  if (warp == 0) {
+    Segment s;
+    long long number = 0;
+    const bool found = find_segment(a, p.m, p.segments, blockIdx.x / a.heads, false, &s, &number);
+    if (lane == 0) sm.seg = s, sm.number = number, sm.found = found, sm.dead = 0;
+    if (!LOCAL && blockIdx.x == 0) {  // bad pairs of cu_seqlens are reported once
+      bool bad = false;
+      long long all = 0;
+      for (long long i = lane; i < a.seqs; i += 32) {
+        const long long b = a.cu[i], e = a.cu[i + 1];
+        if (seq_ok(a, b, e))
+          all += seg_count(e - b, p.m);
+        else
+          bad = true;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (bad || all > p.segments) atomicOr(&g_la_err, KDA_ERR_SEQ);
+    }
+  }
+  __syncthreads();
+  if (!sm.found) return;
+  const Segment sg = sm.seg;
+  const long long number = sm.number;
+  const bool last_seg = sg.index == sg.count - 1;
+  const int slot = a.slots[sg.seq];
+  const long long row0 = sg.begin + (long long)sg.index * p.m * CHUNK;
+  const long long left = sg.end - row0;
+  const int tokens = (int)(left < (long long)p.m * CHUNK ? left : (long long)p.m * CHUNK);
+  const int chunks = (tokens + CHUNK - 1) / CHUNK;
+  if (slot < 0 || slot >= a.pool) {
+    if (!LOCAL && slot == -1) {
+      for (int e = threadIdx.x; e < tokens * (D / 8); e += CHUNK_THREADS)
+        *reinterpret_cast<uint4*>(a.out + (row0 + e / (D / 8)) * a.ldo + h * D + 8 * (e % (D / 8))) =
+            make_uint4(0, 0, 0, 0);
+    } else if (!LOCAL && threadIdx.x == 0) {
+      atomicOr(&g_la_err, KDA_ERR_SLOT);
+    }
+    return;
+  }
+  if (LOCAL && last_seg) return;  // nobody starts from its state
+  const bool resumed = !LOCAL && (sg.count > 1 || (a.has_state && a.has_state[sg.seq]));  // starts from a state
+  unsigned char* pool = static_cast<unsigned char*>(a.state) + ((long long)slot * a.heads + h) * (D * D) * (BF ? 2 : 4);
+  float* wsp = p.ws + (number * a.heads + h) * (D * D);
+  if (!LOCAL && chunks == 0) {  // an empty sequence: its state stays, or is zeros
+    if (!resumed)
+      for (int e = threadIdx.x; e < D * D * (BF ? 2 : 4) / 16; e += CHUNK_THREADS)
+        reinterpret_cast<uint4*>(pool)[e] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+
+  const uint32_t bars = smem_addr(sm.bars);
+  auto bar = [&](int i) { return bars + 8u * i; };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < BARS; ++i)
+      bar_init(bar(i), i >= PAIR ? 2 : i >= KP ? 8 : i == EMPTY_K ? (LOCAL ? 8 : 9) : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (!LOCAL) prefetch_map(&tq);
+    prefetch_map(&tk);
+    prefetch_map(&tv);
+  }
+  if (warp == 9) tmem_alloc(smem_addr(&sm.tmem), 512);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
+  const uint32_t t_sc = tmem, t_os = tmem + 128, t_op = tmem + 256, t_ds = tmem + 384;
+  volatile int* dead = &sm.dead;
+  auto wait = [&](int i, unsigned ph) { return warp_wait(bar(i), ph, dead); };  // whole warps only
+  // the state behind the segment's last chunk is wanted: by the pool, or (LOCAL) by the join
+  const bool want_last = LOCAL || last_seg;
+  bool ok = true;
+
+  if (warp < 8) {
+    const int quarter = warp & 3, half = warp >> 2;
+    const int r = quarter * 32 + lane;  // this thread's row of every accumulator: token i, or v
+    const uint32_t lane_at = (uint32_t)(quarter * 32) << 16;
+    float S[64];  // S[v = r][k = 64 half ..]
+    if (resumed) {
+      if (!LOCAL && sg.count > 1) {
+        const float4* f = reinterpret_cast<const float4*>(wsp + r * D + 64 * half);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 x = __ldcs(f + i);
+          S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
+        }
+      } else if (BF) {
+        const uint4* f = reinterpret_cast<const uint4*>(pool) + (r * D + 64 * half) / 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 x = f[i];
+          S[8 * i] = bf_lo(x.x), S[8 * i + 1] = bf_hi(x.x), S[8 * i + 2] = bf_lo(x.y), S[8 * i + 3] = bf_hi(x.y);
+          S[8 * i + 4] = bf_lo(x.z), S[8 * i + 5] = bf_hi(x.z), S[8 * i + 6] = bf_lo(x.w), S[8 * i + 7] = bf_hi(x.w);
+        }
+      } else {
+        const float4* f = reinterpret_cast<const float4*>(pool) + (r * D + 64 * half) / 4;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 x = f[i];
+          S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) S[i] = 0.0f;
+    }
+    // S as the bf16 operand of Q S^T: [v][k], 64 k a box
+    auto put_state = [&]() {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        sts128(ss + half * BOX + swz128(r, c),
+               make_uint4(pack_bf(S[8 * c], S[8 * c + 1]), pack_bf(S[8 * c + 2], S[8 * c + 3]),
+                          pack_bf(S[8 * c + 4], S[8 * c + 5]), pack_bf(S[8 * c + 6], S[8 * c + 7])));
+      fence_async();
+    };
+    auto arrive = [&](int i) {
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(i));
+    };
+    if (!LOCAL) {
+      put_state();
+      arrive(S_IN);
+    }
+    float seg_decay = 0.0f;
+    for (int c = 0; c < chunks; ++c) {
+      const unsigned ph = c & 1;
+      const int n = tokens - c * CHUNK < CHUNK ? tokens - c * CHUNK : CHUNK;  // tokens of this chunk
+      const bool want = want_last || c + 1 < chunks;
+      // K' = hi + mid + lo, token r, 64 k
+      if (!(ok = wait(DECAY, ph) && wait(FULL_K, ph))) break;
+      const float w = sm.W[r];
+      float total = sm.total;
+      if (want) {
+#pragma unroll 2
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint32_t at = half * BOX + swz128(r, ch);
+          const uint4 u = lds128(sk + at);
+          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+          uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // rows behind the sequence's end are somebody else's: not even times zero
+            float f0 = r < n ? bf_lo(x[j]) * w : 0.0f, f1 = r < n ? bf_hi(x[j]) * w : 0.0f;
+            hi[j] = pack_bf(f0, f1);
+            f0 -= bf_lo(hi[j]), f1 -= bf_hi(hi[j]);
+            mid[j] = pack_bf(f0, f1);
+            f0 -= bf_lo(mid[j]), f1 -= bf_hi(mid[j]);
+            lo[j] = pack_bf(f0, f1);
+          }
+          sts128(skp + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+          sts128(skp + TILE + at, make_uint4(mid[0], mid[1], mid[2], mid[3]));
+          if (!BF) sts128(skp + 2 * TILE + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        }
+      }
+      arrive(EMPTY_K);
+      if (n < CHUNK) {  // nor are their values multiplied by the zeros of P and K'
+        if (!(ok = wait(FULL_V, ph))) break;
+        if (r >= n)
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) sts128(sv + half * BOX + swz128(r, ch), make_uint4(0, 0, 0, 0));
+      }
+      fence_async();
+      arrive(KP);
+
+      float eg = 0.0f;
+      if (!LOCAL) {
+        // the scores' lower triangle, decayed: row i = r, columns 64 half ..
+        const float gi = sm.G[r];
+        eg = ex2(gi);
+        if (!(ok = wait(SCORES, ph))) break;
+        tc_after();
+        uint32_t pk[32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int q0 = 64 * half + 32 * q;
+          if (q0 <= quarter * 32 + 31) {
+            uint32_t x[32];
+            tmem_ld32(t_sc + lane_at + q0, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int j0 = q0 + 16 * b;
+              float f[16];
+              if (j0 + 16 <= quarter * 32) {  // all of the block's tokens are before all of the warp's
+                const float s = ex2(gi - sm.G[j0 + 15]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(x[16 * b + j]) * (s * sm.E[j0 + j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  f[j] = j0 + j <= r ? __uint_as_float(x[16 * b + j]) * ex2(gi - sm.G[j0 + j]) : 0.0f;
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) pk[16 * q + 8 * b + j] = pack_bf(f[2 * j], f[2 * j + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[16 * q + i] = 0u;
+          }
+        }
+        // P takes the scores' place: both halves of these lanes have read theirs
+        tc_before();
+        arrive(PAIR + quarter);
+        if (!(ok = wait(PAIR + quarter, ph))) break;
+        tc_after();
+        tmem_st32(t_sc + lane_at + 32 * half, pk);
+        tmem_wait_st();
+        tc_before();
+        arrive(P_IN);
+      }
+
+      if (want) {
+        if (!(ok = wait(DELTA, ph))) break;
+        tc_after();
+        seg_decay += total;
+        total = ex2(total);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t y[32];
+          tmem_ld32(t_ds + lane_at + 64 * half + 32 * q, y);
+          tmem_wait_ld(y);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) S[32 * q + i] = fmaf(total, S[32 * q + i], __uint_as_float(y[i]));
+        }
+        if (!LOCAL && c + 1 < chunks) put_state();
+      }
+      tc_before();
+      if (!LOCAL) arrive(S_IN);
+
+      if (!LOCAL) {
+        if (!(ok = wait(OUT, ph))) break;
+        tc_after();
+        __nv_bfloat16* o = a.out + (row0 + (long long)c * CHUNK + r) * a.ldo + h * D + 64 * half;
+        const bool from_state = resumed || c > 0;
+        eg *= a.scale;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t y[32], z[32];
+          tmem_ld32(t_op + lane_at + 64 * half + 32 * q, y);
+          if (from_state) {
+            tmem_ld32(t_os + lane_at + 64 * half + 32 * q, z);
+            tmem_wait_ld(y, z);
+          } else {
+            tmem_wait_ld(y);
+          }
+          if (r < n) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float f0 = a.scale * __uint_as_float(y[i + 2 * j]), f1 = a.scale * __uint_as_float(y[i + 2 * j + 1]);
+                if (from_state) {
+                  f0 = fmaf(eg, __uint_as_float(z[i + 2 * j]), f0);
+                  f1 = fmaf(eg, __uint_as_float(z[i + 2 * j + 1]), f1);
+                }
+                w4[j] = pack_bf(f0, f1);
+              }
+              *reinterpret_cast<uint4*>(o + 32 * q + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+          }
+        }
+        tc_before();
+        arrive(O_READ);
+      }
+    }
+    if (ok && want_last) {
+      if (LOCAL) {
+        float4* f = reinterpret_cast<float4*>(wsp + r * D + 64 * half);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        if (threadIdx.x == 0) p.decays[number * a.heads + h] = seg_decay;
+      } else if (BF) {
+        uint4* f = reinterpret_cast<uint4*>(pool) + (r * D + 64 * half) / 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          f[i] = make_uint4(pack_bf(S[8 * i], S[8 * i + 1]), pack_bf(S[8 * i + 2], S[8 * i + 3]),
+                            pack_bf(S[8 * i + 4], S[8 * i + 5]), pack_bf(S[8 * i + 6], S[8 * i + 7]));
+      } else {
+        float4* f = reinterpret_cast<float4*>(pool) + (r * D + 64 * half) / 4;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      }
+    }
+  } else if (warp == 8) {  // copies, and the decays (four tokens a lane)
+    for (int c = 0; c < chunks; ++c) {
+      const unsigned prev = (c & 1) ^ 1;  // the phase of chunk c - 1
+      const int row = (int)(row0 + (long long)c * CHUNK);
+      auto load = [&](int full, int empty, uint32_t dst, const CUtensorMap* map, int col) {
+        if (c > 0 && !(ok = wait(empty, prev))) return;
+        if (lane == 0) {
+          bar_expect(bar(full), TILE);
+          tma_load(dst, map, col, row, bar(full));
+          tma_load(dst + BOX, map, col + 64, row, bar(full));
+        }
+        __syncwarp();
+      };
+      load(FULL_K, EMPTY_K, sk, &tk, hk * D);
+      if (!LOCAL && ok) load(FULL_Q, EMPTY_Q, sq, &tq, hk * D);
+      if (!ok) break;
+      const long long t0 = row0 + (long long)c * CHUNK + 4 * lane;
+      const int n = tokens - c * CHUNK;
+      float g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = 4 * lane + j < n ? a.g[(t0 + j) * a.ldg + h] : 0.0f;
+        g[j] = (x < G_MIN ? G_MIN : x) * LOG2E;
+      }
+      float pre[4], suf[4];  // sums up to and behind each token, each from its own end: the near ones exact
+      pre[0] = g[0], pre[1] = pre[0] + g[1], pre[2] = pre[1] + g[2], pre[3] = pre[2] + g[3];
+      suf[3] = 0.0f, suf[2] = g[3], suf[1] = suf[2] + g[2], suf[0] = suf[1] + g[1];
+      float up = pre[3], down = suf[0] + g[0];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(0xffffffffu, up, o), y = __shfl_down_sync(0xffffffffu, down, o);
+        if (lane >= o) up += x;
+        if (lane + o < 32) down += y;
+      }
+      float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+      if (lane == 0) before = 0.0f;
+      if (lane == 31) behind = 0.0f;
+      const float total = __shfl_sync(0xffffffffu, down, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pre[j] += before, suf[j] += behind;
+      const float ref = __shfl_sync(0xffffffffu, pre[3], lane | 3);
+      // the arrays' readers are done with the chunk before
+      if (c > 0 && !(ok = wait(LOCAL ? KP : P_IN, prev))) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sm.G[4 * lane + j] = pre[j];
+        sm.W[4 * lane + j] = ex2(suf[j]);
+        sm.E[4 * lane + j] = ex2(ref - pre[j]);
+      }
+      if (lane == 0) sm.total = total;
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(DECAY));
+      // (the last of a chunk's operands to come free)
+      load(FULL_V, EMPTY_V, sv, &tv, h * D);
+      if (!ok) break;
+    }
+  } else if (warp == 9) {  // matrix products
+    for (int c = 0; c < chunks; ++c) {
+      const unsigned ph = c & 1;
+      const bool want = want_last || c + 1 < chunks;
+      if (!LOCAL) {
+        if (!(ok = wait(FULL_Q, ph) && wait(FULL_K, ph))) break;
+        tc_after();
+        if (lane == 0) {
+          constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t at = (k >> 2) * BOX + 32 * (k & 3);
+            mma_ss(t_sc, desc_k(sq + at), desc_k(sk + at), id, k > 0);
+          }
+          mma_commit(bar(SCORES));
+          mma_commit(bar(EMPTY_K));
+        }
+        __syncwarp();
+        const bool from_state = resumed || c > 0;
+        if (!(ok = wait(S_IN, ph) && (c == 0 || wait(O_READ, ph ^ 1)))) break;
+        tc_after();
+        if (lane == 0) {
+          if (from_state) {
+            constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t at = (k >> 2) * BOX + 32 * (k & 3);
+              mma_ss(t_os, desc_k(sq + at), desc_k(ss + at), id, k > 0);
+            }
+          }
+          mma_commit(bar(EMPTY_Q));
+        }
+        __syncwarp();
+      }
+      if (!(ok = wait(KP, ph) && wait(FULL_V, ph))) break;
+      tc_after();
+      if (lane == 0 && want) {
+        constexpr uint32_t id = idesc_bf16(128, 128, true, true);
+#pragma unroll
+        for (int part = BF ? 1 : 2; part >= 0; --part)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ss(t_ds, desc_mn(sv + 2048 * k, BOX), desc_mn(skp + part * TILE + 2048 * k, BOX), id,
+                   part < (BF ? 1 : 2) || k > 0);
+        if (LOCAL) mma_commit(bar(EMPTY_V));
+        mma_commit(bar(DELTA));
+      }
+      __syncwarp();
+      if (!LOCAL) {
+        if (!(ok = wait(P_IN, ph))) break;
+        tc_after();
+        if (lane == 0) {
+          constexpr uint32_t id = idesc_bf16(128, 128, false, true);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mma_ts(t_op, t_sc + 8 * k, desc_mn(sv + 2048 * k, BOX), id, k > 0);
+          mma_commit(bar(EMPTY_V));
+          mma_commit(bar(OUT));
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (!ok) {
+    *dead = 1;
+    if (lane == 0) atomicOr(&g_la_err, KDA_ERR_TIMEOUT);
+  }
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (*dead && threadIdx.x == 9 * 32) {
+    // what is still in flight lands before the memory goes: the MMAs, then the copies nobody has
+    // waited for (they take microseconds; ~10 ms)
+    int never = 0;
+    mma_commit(bar(DRAIN));
+    bar_wait(bar(DRAIN), 0, &never);
+    const long long c0 = clock64();
+    while (clock64() - c0 < 20000000ll) {
+    }
+  }
+  __syncthreads();
+  if (warp == 9) tmem_free(tmem, 512);
+}
+
+// From the segments' own states to the states they start from, elementwise: 1/4 of
+// a state a CTA, in place in the workspace.
+template <bool BF>
+__global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
+  const LaArgs& a = p.a;
+  __shared__ Segment s_seg;
+  __shared__ long long s_number;
+  __shared__ int s_found;
+  const long long task = blockIdx.x / 4;
+  const long long seq = task / a.heads;
+  const int h = (int)(task % a.heads);
+  {
+    const long long b = a.cu[seq], e = a.cu[seq + 1];
+    if (!seq_ok(a, b, e) || seg_count(e - b, p.m) < 2) return;
+  }
+  if (threadIdx.x < 32) {
+    Segment s;
+    long long number = 0;
+    const bool found = find_segment(a, p.m, p.segments, seq, true, &s, &number);
+    if (threadIdx.x == 0) s_seg = s, s_number = number, s_found = found;
+  }
+  __syncthreads();
+  if (!s_found) return;
+  const int slot = a.slots[seq];
+  if (slot < 0 || slot >= a.pool) return;
+  const int count = s_seg.count;
+  const long long at = (long long)(blockIdx.x % 4) * (D * D / 4) + 4 * threadIdx.x;  // + 1024 i
+  const bool has = a.has_state && a.has_state[seq];
+  float4 S[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long e = ((long long)slot * a.heads + h) * (D * D) + at + 1024 * i;
+    S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (has && BF) {
+      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.state) + e);
+      S[i] = make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
+    } else if (has) {
+      S[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.state) + e);
+    }
+  }
+  const long long step = (long long)a.heads * D * D;
+  float4* w = reinterpret_cast<float4*>(p.ws + (s_number * a.heads + h) * (D * D) + at);
+  const float* d = p.decays + s_number * a.heads + h;
+  for (int s = 0; s < count; ++s, w += step / 4, d += a.heads) {
+    const bool more = s + 1 < count;
+    float4 own[4];
+    float f = 0.0f;
+    if (more) {
+      f = ex2(*d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = w[256 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[256 * i] = S[i];
+      if (more)
+        S[i] = make_float4(fmaf(f, S[i].x, own[i].x), fmaf(f, S[i].y, own[i].y), fmaf(f, S[i].z, own[i].z),
+                           fmaf(f, S[i].w, own[i].w));
+    }
+  }
+}
 
 // The checks that step and prefill share.  Without rows (a prompt call of empty
 // sequences) there is nothing behind the rows' pointers.
@@ -235,8 +802,8 @@ bool la_args_ok(long long rows, const void* q, long long ldq, const void* k, lon
   const long long nq = (long long)qk_heads * D, nv = (long long)heads * D;
   if (ldq < nq || ldk < nq || ldv < nv || ldo < nv || ldq % 8 || ldk % 8 || ldv % 8 || ldo % 8) return false;
   if (ldg != 0 && ldg < heads) return false;
-  return aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && aligned(out, 16) && aligned(state, 16) &&
-         aligned(g, 4) && aligned(slots, 4);
+  return ptr_aligned(q, 16) && ptr_aligned(k, 16) && ptr_aligned(v, 16) && ptr_aligned(out, 16) && ptr_aligned(state, 16) &&
+         ptr_aligned(g, 4) && ptr_aligned(slots, 4);
 }
 
 LaArgs la_args(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
@@ -280,9 +847,82 @@ extern "C" int kda_la_step(const void* q, long long ldq, const void* k, long lon
   return launched();
 }
 
+namespace {
+
+// How a prompt call is cut: chunks a segment, and the segments there can be at most.
+struct Cut {
+  int m;
+  long long segments;
+  bool split;  // some sequence may have several segments
+};
+
+// Times in us: a chunk of a segment, a segment's fixed part; the same for the pass over
+// the segments' own states; the join.
+constexpr double T_CHUNK = 1.9, T_FIXED = 5.0, T_OWN = 1.3, T_OWN_FIXED = 5.0, T_JOIN = 4.0;
+
+Cut la_cut(long long rows, int heads, long long seqs, long long max_len, int sms) {
+  const long long longest = (max_len < rows ? max_len : rows) / CHUNK + 1;  // chunks, about
+  const double chunks = (double)rows / CHUNK + 0.5 * (double)seqs;
+  Cut best = {};
+  double least = 1e300;
+  for (long long m = 1;; m = m < 8 ? m + 1 : m + m / 8) {
+    const bool last = m >= longest;
+    if (last) m = longest;
+    const double segs = chunks / (double)m > (double)seqs ? chunks / (double)m : (double)seqs;
+    const double per = chunks / segs;  // chunks of a segment on average
+    const double w = segs * heads / sms;
+    const double waves = w <= 1.0 ? 1.0 : (double)(long long)(w + 0.999);
+    const double run = per * waves > (double)m ? per * waves : (double)m;
+    double t = run * T_CHUNK + waves * T_FIXED;
+    if (!last) t += run * T_OWN + waves * T_OWN_FIXED + T_JOIN;
+    if (t < least * 0.999) {
+      least = t;
+      best.m = (int)(m > 0x1000000 ? 0x1000000 : m);
+      best.split = !last;
+    }
+    if (last) break;
+  }
+  const long long per = (long long)best.m * CHUNK;
+  best.segments = rows / per + seqs;
+  return best;
+}
+
+bool la_sizes_ok(long long rows, int heads, long long seqs, long long max_len) {
+  return rows >= 0 && rows <= 0x7fffffffLL && heads >= 1 && heads <= 65535 && seqs >= 0 && seqs <= 0x7fffffffLL &&
+         max_len >= 0;
+}
+
+template <bool BF>
+int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& p,
+                      const Cut& cut, cudaStream_t st) {
+  const unsigned grid = (unsigned)(cut.segments * p.a.heads);
+  // the shared-memory attribute is per device and cheap: set on every call
+  if (cudaFuncSetAttribute(la_chunk_kernel<BF, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
+      cudaSuccess)
+    return KDA_ECUDA;
+  if (cut.split) {
+    // (the workspace is fp32 whatever the pool)
+    if (cudaFuncSetAttribute(la_chunk_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
+        cudaSuccess)
+      return KDA_ECUDA;
+    la_chunk_kernel<false, true><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, p);
+    la_join_kernel<BF><<<(unsigned)(p.a.seqs * p.a.heads * 4), 256, 0, st>>>(p);
+  }
+  la_chunk_kernel<BF, false><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, p);
+  return launched();
+}
+
+}  // namespace
+
 extern "C" long long kda_la_prefill_workspace(long long rows, int heads, long long seqs, long long max_len) {
-  (void)rows, (void)heads, (void)seqs, (void)max_len;
-  return 0;
+  if (!la_sizes_ok(rows, heads, seqs, max_len) || seqs == 0) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return 0;
+  const Cut cut = la_cut(rows, heads, seqs, max_len, sms);
+  if (!cut.split) return 0;
+  return (cut.segments * heads * (D * D + 1) * 4 + 15) / 16 * 16;
 }
 
 extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long long ldk, const void* v,
@@ -291,25 +931,41 @@ extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long 
                               const int* has_state, void* state_pool, int state_dtype, long long pool_slots,
                               const int* slots, void* out, long long ldo, void* workspace, long long workspace_bytes,
                               void* cuda_stream) {
-  if (rows < 0 || rows > 0x7fffffffLL || seqs < 0 || max_len < 0) return KDA_EINVAL;
+  if (!la_sizes_ok(rows, heads, seqs, max_len)) return KDA_EINVAL;
   if (seqs == 0) return KDA_OK;
   if (!la_args_ok(rows, q, ldq, k, ldk, v, ldv, heads, qk_heads, g, ldg, state_pool, state_dtype, pool_slots, slots,
                   out, ldo) ||
-      !cu_seqlens || !aligned(cu_seqlens, 4) || !aligned(has_state, 4))
+      !cu_seqlens || !ptr_aligned(cu_seqlens, 4) || !ptr_aligned(has_state, 4))
     return KDA_EINVAL;
-  if (seqs > 0x7fffffffLL / STEP_SPLIT / heads) return KDA_EINVAL;
-  const long long need = kda_la_prefill_workspace(rows, heads, seqs, max_len);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return KDA_EINVAL;
-  LaArgs a = la_args(q, ldq, k, ldk, v, ldv, rows, heads, qk_heads, g, ldg, scale, state_pool, pool_slots, slots,
-                     out, ldo);
-  a.cu = cu_seqlens, a.has_state = has_state, a.seqs = seqs, a.max_len = max_len;
-  const unsigned grid = (unsigned)(seqs * heads * STEP_SPLIT);
+  // the largest grids: a CTA a segment and head, four a sequence and head
+  if ((rows / CHUNK + seqs) > 0x7fffffffLL / heads || seqs > 0x7fffffffLL / 4 / heads) return KDA_EINVAL;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ECUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return KDA_ECUDA;
+  const Cut cut = la_cut(rows, heads, seqs, max_len, sms);
+  const long long need = cut.split ? (cut.segments * heads * (D * D + 1) * 4 + 15) / 16 * 16 : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need || !ptr_aligned(workspace, 16))) return KDA_EINVAL;
+  CUtensorMap tq = {}, tk = {}, tv = {};
+  if (rows > 0) {
+    if (!on_device(q, dev) || !on_device(k, dev) || !on_device(v, dev)) return KDA_EINVAL;
+    const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle s = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!encode_2d(&tq, t, q, rows, (long long)qk_heads * D, ldq * 2, 64, CHUNK, s) ||
+        !encode_2d(&tk, t, k, rows, (long long)qk_heads * D, ldk * 2, 64, CHUNK, s) ||
+        !encode_2d(&tv, t, v, rows, (long long)heads * D, ldv * 2, 64, CHUNK, s))
+      return KDA_ECUDA;
+  }
+  ChunkArgs p;
+  p.a = la_args(q, ldq, k, ldk, v, ldv, rows, heads, qk_heads, g, ldg, scale, state_pool, pool_slots, slots, out, ldo);
+  p.a.cu = cu_seqlens, p.a.has_state = has_state, p.a.seqs = seqs, p.a.max_len = max_len;
+  p.ws = static_cast<float*>(workspace);
+  p.decays = p.ws + cut.segments * heads * (D * D);
+  p.m = cut.m;
+  p.segments = cut.segments;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (state_dtype == KDA_STATE_BF16)
-    la_scan_kernel<true><<<grid, 32 * STEP_WARPS, 0, st>>>(a);
-  else
-    la_scan_kernel<false><<<grid, 32 * STEP_WARPS, 0, st>>>(a);
-  return launched();
+  return state_dtype == KDA_STATE_BF16 ? la_prefill_launch<true>(tq, tk, tv, p, cut, st)
+                                       : la_prefill_launch<false>(tq, tk, tv, p, cut, st);
 }
 
 extern "C" int kda_la_check(void* cuda_stream, unsigned* device_flags) {
