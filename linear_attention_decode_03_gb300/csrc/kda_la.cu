@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 // bits; hi + mid where the pool is bf16), smallest first, each chunk's sum added to S
 // in fp32 registers, so that nothing accumulates in the tensor pipe over chunks.
 //
-// Roles (warps): 0-7 compute, 8 TMA copies and the decays, 9 MMAs.  Per chunk
+// Roles (warps): 0-15 compute, 16 TMA copies and the decays, 17 MMAs.  Per chunk
 //   MMA:      QK, QS          | V^T K'            | PV
 //   compute:  K -> K'  | scores -> P | S += V^T K', its bf16 | outputs
 // and the copies of the next chunk's Q, K and V go out as soon as this one's last reader is done.
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 constexpr int CHUNK = 128;
 constexpr int BOX = 64 * 128 * 2;          // 64 columns of 128 rows, bf16
 constexpr int TILE = 2 * BOX;              // a 128 x 128 bf16 operand
-constexpr int COMPUTE = 256;               // threads of the compute warps
-constexpr int CHUNK_THREADS = COMPUTE + 64;
+constexpr int COMPUTE_WARPS = 16;          // four for each quarter of an accumulator's 128 rows
+constexpr int CHUNK_THREADS = 32 * (COMPUTE_WARPS + 2);
 constexpr int MISC = 2048;                 // ChunkMisc
 constexpr int CHUNK_SMEM = 7 * TILE + MISC + 1024;  // (1024: the alignment of the swizzled tiles)
 static_assert(CHUNK_SMEM <= 227 * 1024, "shared memory of one CTA");
@@ -275,9 +275,9 @@ struct ChunkArgs {
 
 enum {  // barriers: completed by copies and MMAs (one arrival), ...
   FULL_Q, FULL_K, FULL_V, EMPTY_Q, EMPTY_V, SCORES, DELTA, OUT, DRAIN, DECAY,
-  EMPTY_K,                     // ... by the 8 compute warps (and QK's commit), ...
-  KP, P_IN, S_IN, O_READ,      // ... by the 8 compute warps, ...
-  PAIR, BARS = PAIR + 4        // ... by the two warps of a quarter of the rows
+  EMPTY_K,                   // ... by the compute warps (and QK's commit), ...
+  KP, P_IN, S_IN, O_READ,    // ... by the compute warps, ...
+  QUARTER, BARS = QUARTER + 4  // ... by the four warps of a quarter of the rows
 };
 struct ChunkMisc {
   float G[CHUNK];  // G_i (log2)
@@ -359,13 +359,13 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < BARS; ++i)
-      bar_init(bar(i), i >= PAIR ? 2 : i >= KP ? 8 : i == EMPTY_K ? (LOCAL ? 8 : 9) : 1);
+      bar_init(bar(i), i >= QUARTER ? 4 : i >= KP ? COMPUTE_WARPS : i == EMPTY_K ? COMPUTE_WARPS + (LOCAL ? 0 : 1) : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (!LOCAL) prefetch_map(&tq);
     prefetch_map(&tk);
     prefetch_map(&tv);
   }
-  if (warp == 9) tmem_alloc(smem_addr(&sm.tmem), 512);
+  if (warp == COMPUTE_WARPS + 1) tmem_alloc(smem_addr(&sm.tmem), 512);
   tc_before();
   __syncthreads();
   tc_after();
@@ -377,44 +377,41 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   const bool want_last = LOCAL || last_seg;
   bool ok = true;
 
-  if (warp < 8) {
-    const int quarter = warp & 3, half = warp >> 2;
-    const int r = quarter * 32 + lane;  // this thread's row of every accumulator: token i, or v
+  if (warp < COMPUTE_WARPS) {
+    const int quarter = warp & 3, part = warp >> 2;
+    const int r = quarter * 32 + lane;  // this thread's row of every accumulator and tile: a token, or a v ...
+    const int c0 = 32 * part;           // ... and its 32 columns
     const uint32_t lane_at = (uint32_t)(quarter * 32) << 16;
-    float S[64];  // S[v = r][k = 64 half ..]
+    // 16-byte chunk i (0..3) of these columns in a 128-byte-swizzled tile of bf16
+    auto chunk_at = [&](int i) { return (part >> 1) * BOX + swz128(r, 4 * (part & 1) + i); };
+    float S[32];  // S[v = r][k = c0 ..]
     if (resumed) {
-      if (!LOCAL && sg.count > 1) {
-        const float4* f = reinterpret_cast<const float4*>(wsp + r * D + 64 * half);
+      if (BF && sg.count == 1) {
+        const uint4* f = reinterpret_cast<const uint4*>(pool) + (r * D + c0) / 8;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float4 x = __ldcs(f + i);
-          S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
-        }
-      } else if (BF) {
-        const uint4* f = reinterpret_cast<const uint4*>(pool) + (r * D + 64 * half) / 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const uint4 x = f[i];
           S[8 * i] = bf_lo(x.x), S[8 * i + 1] = bf_hi(x.x), S[8 * i + 2] = bf_lo(x.y), S[8 * i + 3] = bf_hi(x.y);
           S[8 * i + 4] = bf_lo(x.z), S[8 * i + 5] = bf_hi(x.z), S[8 * i + 6] = bf_lo(x.w), S[8 * i + 7] = bf_hi(x.w);
         }
       } else {
-        const float4* f = reinterpret_cast<const float4*>(pool) + (r * D + 64 * half) / 4;
+        const float4* f = reinterpret_cast<const float4*>(sg.count > 1 ? reinterpret_cast<unsigned char*>(wsp) : pool) +
+                          (r * D + c0) / 4;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const float4 x = f[i];
           S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) S[i] = 0.0f;
+      for (int i = 0; i < 32; ++i) S[i] = 0.0f;
     }
     // S as the bf16 operand of Q S^T: [v][k], 64 k a box
     auto put_state = [&]() {
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        sts128(ss + half * BOX + swz128(r, c),
+      for (int c = 0; c < 4; ++c)
+        sts128(ss + chunk_at(c),
                make_uint4(pack_bf(S[8 * c], S[8 * c + 1]), pack_bf(S[8 * c + 2], S[8 * c + 3]),
                           pack_bf(S[8 * c + 4], S[8 * c + 5]), pack_bf(S[8 * c + 6], S[8 * c + 7])));
       fence_async();
@@ -432,14 +429,14 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       const unsigned ph = c & 1;
       const int n = tokens - c * CHUNK < CHUNK ? tokens - c * CHUNK : CHUNK;  // tokens of this chunk
       const bool want = want_last || c + 1 < chunks;
-      // K' = hi + mid + lo, token r, 64 k
+      // K' = hi + mid + lo, token r
       if (!(ok = wait(DECAY, ph) && wait(FULL_K, ph))) break;
       const float w = sm.W[r];
       float total = sm.total;
       if (want) {
-#pragma unroll 2
-        for (int ch = 0; ch < 8; ++ch) {
-          const uint32_t at = half * BOX + swz128(r, ch);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          const uint32_t at = chunk_at(ch);
           const uint4 u = lds128(sk + at);
           const uint32_t x[4] = {u.x, u.y, u.z, u.w};
           uint32_t hi[4], mid[4], lo[4];
@@ -463,53 +460,49 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         if (!(ok = wait(FULL_V, ph))) break;
         if (r >= n)
 #pragma unroll
-          for (int ch = 0; ch < 8; ++ch) sts128(sv + half * BOX + swz128(r, ch), make_uint4(0, 0, 0, 0));
+          for (int ch = 0; ch < 4; ++ch) sts128(sv + chunk_at(ch), make_uint4(0, 0, 0, 0));
       }
       fence_async();
       arrive(KP);
 
       float eg = 0.0f;
       if (!LOCAL) {
-        // the scores' lower triangle, decayed: row i = r, columns 64 half ..
+        // the scores' lower triangle, decayed: row i = r
         const float gi = sm.G[r];
         eg = ex2(gi);
         if (!(ok = wait(SCORES, ph))) break;
         tc_after();
-        uint32_t pk[32];
+        uint32_t pk[16];
+        if (part <= quarter) {
+          uint32_t x[32];
+          tmem_ld(t_sc + lane_at + c0, x);
+          tmem_wait_ld(x);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int q0 = 64 * half + 32 * q;
-          if (q0 <= quarter * 32 + 31) {
-            uint32_t x[32];
-            tmem_ld32(t_sc + lane_at + q0, x);
-            tmem_wait_ld(x);
+          for (int b = 0; b < 2; ++b) {
+            const int j0 = c0 + 16 * b;
+            float f[16];
+            if (part < quarter) {  // all of the block's tokens are before all of the warp's
+              const float s = ex2(gi - sm.G[j0 + 15]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int j0 = q0 + 16 * b;
-              float f[16];
-              if (j0 + 16 <= quarter * 32) {  // all of the block's tokens are before all of the warp's
-                const float s = ex2(gi - sm.G[j0 + 15]);
+              for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(x[16 * b + j]) * (s * sm.E[j0 + j]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(x[16 * b + j]) * (s * sm.E[j0 + j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  f[j] = j0 + j <= r ? __uint_as_float(x[16 * b + j]) * ex2(gi - sm.G[j0 + j]) : 0.0f;
-              }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) pk[16 * q + 8 * b + j] = pack_bf(f[2 * j], f[2 * j + 1]);
+              for (int j = 0; j < 16; ++j)
+                f[j] = j0 + j <= r ? __uint_as_float(x[16 * b + j]) * ex2(gi - sm.G[j0 + j]) : 0.0f;
             }
-          } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[16 * q + i] = 0u;
+            for (int j = 0; j < 8; ++j) pk[8 * b + j] = pack_bf(f[2 * j], f[2 * j + 1]);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 0u;
         }
-        // P takes the scores' place: both halves of these lanes have read theirs
+        // P takes the scores' place, once all four warps of these lanes have read theirs
         tc_before();
-        arrive(PAIR + quarter);
-        if (!(ok = wait(PAIR + quarter, ph))) break;
+        arrive(QUARTER + quarter);
+        if (!(ok = wait(QUARTER + quarter, ph))) break;
         tc_after();
-        tmem_st32(t_sc + lane_at + 32 * half, pk);
+        tmem_st(t_sc + lane_at + 16 * part, pk);
         tmem_wait_st();
         tc_before();
         arrive(P_IN);
@@ -520,14 +513,11 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         tc_after();
         seg_decay += total;
         total = ex2(total);
+        uint32_t y[32];
+        tmem_ld(t_ds + lane_at + c0, y);
+        tmem_wait_ld(y);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t y[32];
-          tmem_ld32(t_ds + lane_at + 64 * half + 32 * q, y);
-          tmem_wait_ld(y);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) S[32 * q + i] = fmaf(total, S[32 * q + i], __uint_as_float(y[i]));
-        }
+        for (int i = 0; i < 32; ++i) S[i] = fmaf(total, S[i], __uint_as_float(y[i]));
         if (!LOCAL && c + 1 < chunks) put_state();
       }
       tc_before();
@@ -536,59 +526,61 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       if (!LOCAL) {
         if (!(ok = wait(OUT, ph))) break;
         tc_after();
-        __nv_bfloat16* o = a.out + (row0 + (long long)c * CHUNK + r) * a.ldo + h * D + 64 * half;
         const bool from_state = resumed || c > 0;
         eg *= a.scale;
+        // by way of shared memory (this warp's own part of K', which nobody reads now), so that
+        // the stores are rows' 64 bytes together
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t y[32], z[32];
-          tmem_ld32(t_op + lane_at + 64 * half + 32 * q, y);
+          uint32_t y[16], z[16];
+          tmem_ld(t_op + lane_at + c0 + 16 * q, y);
           if (from_state) {
-            tmem_ld32(t_os + lane_at + 64 * half + 32 * q, z);
+            tmem_ld(t_os + lane_at + c0 + 16 * q, z);
             tmem_wait_ld(y, z);
           } else {
             tmem_wait_ld(y);
           }
-          if (r < n) {
+          uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w4[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float f0 = a.scale * __uint_as_float(y[i + 2 * j]), f1 = a.scale * __uint_as_float(y[i + 2 * j + 1]);
-                if (from_state) {
-                  f0 = fmaf(eg, __uint_as_float(z[i + 2 * j]), f0);
-                  f1 = fmaf(eg, __uint_as_float(z[i + 2 * j + 1]), f1);
-                }
-                w4[j] = pack_bf(f0, f1);
-              }
-              *reinterpret_cast<uint4*>(o + 32 * q + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          for (int j = 0; j < 8; ++j) {
+            float f0 = a.scale * __uint_as_float(y[2 * j]), f1 = a.scale * __uint_as_float(y[2 * j + 1]);
+            if (from_state) {
+              f0 = fmaf(eg, __uint_as_float(z[2 * j]), f0);
+              f1 = fmaf(eg, __uint_as_float(z[2 * j + 1]), f1);
             }
+            w[j] = pack_bf(f0, f1);
           }
+          sts128(skp + chunk_at(2 * q), make_uint4(w[0], w[1], w[2], w[3]));
+          sts128(skp + chunk_at(2 * q + 1), make_uint4(w[4], w[5], w[6], w[7]));
         }
+        __syncwarp();
+        __nv_bfloat16* o = a.out + (row0 + (long long)c * CHUNK + quarter * 32) * a.ldo + h * D + c0 + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 8 * i + (lane >> 2);
+          const uint4 u = lds128(skp + (part >> 1) * BOX + swz128(quarter * 32 + t, 4 * (part & 1) + (lane & 3)));
+          if (quarter * 32 + t < n) *reinterpret_cast<uint4*>(o + t * a.ldo) = u;
+        }
+        __syncwarp();  // before K' goes there again
         tc_before();
         arrive(O_READ);
       }
     }
     if (ok && want_last) {
-      if (LOCAL) {
-        float4* f = reinterpret_cast<float4*>(wsp + r * D + 64 * half);
+      if (BF) {
+        uint4* f = reinterpret_cast<uint4*>(pool) + (r * D + c0) / 8;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-        if (threadIdx.x == 0) p.decays[number * a.heads + h] = seg_decay;
-      } else if (BF) {
-        uint4* f = reinterpret_cast<uint4*>(pool) + (r * D + 64 * half) / 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           f[i] = make_uint4(pack_bf(S[8 * i], S[8 * i + 1]), pack_bf(S[8 * i + 2], S[8 * i + 3]),
                             pack_bf(S[8 * i + 4], S[8 * i + 5]), pack_bf(S[8 * i + 6], S[8 * i + 7]));
       } else {
-        float4* f = reinterpret_cast<float4*>(pool) + (r * D + 64 * half) / 4;
+        float4* f = reinterpret_cast<float4*>(LOCAL ? reinterpret_cast<unsigned char*>(wsp) : pool) + (r * D + c0) / 4;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        for (int i = 0; i < 8; ++i) f[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        if (LOCAL && threadIdx.x == 0) p.decays[number * a.heads + h] = seg_decay;
       }
     }
-  } else if (warp == 8) {  // copies, and the decays (four tokens a lane)
+  } else if (warp == COMPUTE_WARPS) {  // copies, and the decays (four tokens a lane)
     for (int c = 0; c < chunks; ++c) {
       const unsigned prev = (c & 1) ^ 1;  // the phase of chunk c - 1
       const int row = (int)(row0 + (long long)c * CHUNK);
@@ -644,7 +636,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       load(FULL_V, EMPTY_V, sv, &tv, h * D);
       if (!ok) break;
     }
-  } else if (warp == 9) {  // matrix products
+  } else {  // matrix products
     for (int c = 0; c < chunks; ++c) {
       const unsigned ph = c & 1;
       const bool want = want_last || c + 1 < chunks;
@@ -714,7 +706,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (*dead && threadIdx.x == 9 * 32) {
+  if (*dead && threadIdx.x == 32 * (COMPUTE_WARPS + 1)) {
     // what is still in flight lands before the memory goes: the MMAs, then the copies nobody has
     // waited for (they take microseconds; ~10 ms)
     int never = 0;
@@ -725,7 +717,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     }
   }
   __syncthreads();
-  if (warp == 9) tmem_free(tmem, 512);
+  if (warp == COMPUTE_WARPS + 1) tmem_free(tmem, 512);
 }
 
 // From the segments' own states to the states they start from, elementwise: 1/4 of

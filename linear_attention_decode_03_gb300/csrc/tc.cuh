@@ -133,15 +133,17 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // the loads into these registers are done (the empty statements tie their uses behind the wait)
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32], uint32_t (&w)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N], uint32_t (&w)[N]) {
   tmem_wait_ld(v);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(w[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(w[i]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // `cols` (a power of two >= 32) columns of tensor memory, by one whole warp; the address goes to *slot
@@ -152,8 +154,16 @@ __device__ __forceinline__ void tmem_alloc(uint32_t slot, unsigned cols) {
 __device__ __forceinline__ void tmem_free(uint32_t tmem, unsigned cols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
-// 32 columns of the warp's 32 lanes (its quarter of the 128: 32 (warp % 4)); no wait
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&v)[32]) {
+// 16 or 32 columns of the warp's 32 lanes (its quarter of the 128: 32 (warp % 4)); no wait
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -163,14 +173,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&v)[32]) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(a));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(a),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
