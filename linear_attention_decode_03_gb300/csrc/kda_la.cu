@@ -177,20 +177,23 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 //   o_i = scale (e^{G_i} S q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
 //   S'  = e^{G_C} S + sum_j v_j (e^{R_j} k_j)^T
 // so a chunk is matrix products: scores Q K^T, their decayed lower triangle P times V, Q S^T, and
-// V^T K' with K' the decayed keys.  One CTA takes a segment (a run of chunks of one
+// K'^T V with K' the decayed keys.  One CTA takes a segment (a run of chunks of one
 // sequence and head) and carries S from chunk to chunk in fp32 registers; the
-// products run on tcgen05 into four 128-column accumulators, the whole tensor
-// memory.  Every exponent is at most 0.
+// products run on tcgen05.  Every exponent is at most 0.
 //
 // What is rounded: P and, as an operand of Q S^T, S to bf16 (an output of bf16
 // anyway).  The state itself is summed from exact parts: K' = hi + mid + lo in bf16 (24
-// bits; hi + mid where the pool is bf16), smallest first, each chunk's sum added to S
-// in fp32 registers, so that nothing accumulates in the tensor pipe over chunks.
+// bits; hi + mid where the pool is bf16), each chunk's sum added to S in fp32
+// registers, so that nothing accumulates in the tensor pipe over chunks.
 //
-// Roles (warps): 0-15 compute, 16 TMA copies and the decays, 17 MMAs.  Per chunk
-//   MMA:      QK, QS          | V^T K'            | PV
-//   compute:  K -> K'  | scores -> P | S += V^T K', its bf16 | outputs
-// and the copies of the next chunk's Q, K and V go out as soon as this one's last reader is done.
+// What bounds it is shared memory's 128 bytes a cycle: a 128 x 128 x 16 MMA takes 8 KB of
+// operands in its 64 cycles.  So the A operands that threads make themselves, P and K'^T, go
+// to tensor memory: 128 columns of scores that become P (64) and lo (64), 128 of hi and
+// mid, 128 of outputs (Q S^T, scaled there by e^{G_i}, PV added on top), 128 of K'^T V.
+//
+// Roles (warps): 0-15 compute, 16 TMA copies (two stages of Q, K, V) and the decays, 17 MMAs.
+//   MMA:     QK QS | mid, hi | lo PV                | QK ...
+//   compute: scores -> P; QS * e^G | K -> K' of the next chunk | S += K'^T V | outputs
 //
 // A long sequence is split into segments to fill the GPU: la_chunk_kernel<., true> computes
 // each segment's own contribution to the state, la_join_kernel turns these into the states the
@@ -273,11 +276,13 @@ struct ChunkArgs {
   long long segments;  // at most
 };
 
-enum {  // barriers: completed by copies and MMAs (one arrival), ...
-  FULL_Q, FULL_K, FULL_V, EMPTY_Q, EMPTY_V, SCORES, DELTA, OUT, DRAIN, DECAY,
-  EMPTY_K,                   // ... by the compute warps (and QK's commit), ...
-  KP, P_IN, S_IN, O_READ,    // ... by the compute warps, ...
-  QUARTER, BARS = QUARTER + 4  // ... by the four warps of a quarter of the rows
+enum {  // barriers: completed by copies and MMAs (one arrival), two stages of each, ...
+  FULL_Q, FULL_K = FULL_Q + 2, FULL_V = FULL_K + 2, EMPTY_V = FULL_V + 2,
+  SCORES = EMPTY_V + 2, FROM_S, HI_DONE, DELTA, OUT, DRAIN,
+  DECAY_W, DECAY_G,                         // ... by the decays' warp, ...
+  EMPTY_K, EMPTY_Q = EMPTY_K + 2,           // ... by the compute warps (EMPTY_K: and QK's commit), two stages, ...
+  KP = EMPTY_Q + 2, P_IN, S_IN, O_READ,     // ... by the compute warps, ...
+  QUARTER, BARS = QUARTER + 4               // ... by the four warps of a quarter of the rows
 };
 struct ChunkMisc {
   float G[CHUNK];  // G_i (log2)
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   extern __shared__ __align__(1024) unsigned char dyn[];
   // (all shared memory is dynamic: the seven operand tiles leave no room for a second alignment)
   const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = base + TILE, sv = base + 2 * TILE, skp = base + 3 * TILE, ss = base + 6 * TILE;
+  const uint32_t ss = base + 6 * TILE;  // S for Q S^T; before it two stages of Q, K, V
   ChunkMisc& sm = *reinterpret_cast<ChunkMisc*>(dyn + (base - smem_addr(dyn)) + 7 * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = (int)(blockIdx.x % a.heads), hk = h / a.share;
@@ -359,7 +364,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < BARS; ++i)
-      bar_init(bar(i), i >= QUARTER ? 4 : i >= KP ? COMPUTE_WARPS : i == EMPTY_K ? COMPUTE_WARPS + (LOCAL ? 0 : 1) : 1);
+      bar_init(bar(i), i >= QUARTER                                  ? 4
+                       : i == EMPTY_K || i == EMPTY_K + 1 ? COMPUTE_WARPS + (LOCAL ? 0 : 1)
+                       : i >= EMPTY_Q                     ? COMPUTE_WARPS
+                                                          : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (!LOCAL) prefetch_map(&tq);
     prefetch_map(&tk);
@@ -370,7 +378,14 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
-  const uint32_t t_sc = tmem, t_os = tmem + 128, t_op = tmem + 256, t_ds = tmem + 384;
+  // tensor memory: scores, then P and lo; hi and mid; outputs; K'^T V.  (LOCAL: two sets of hi, mid, lo; K'^T V)
+  const uint32_t t_sc = tmem, t_p = tmem, t_o = tmem + 256, t_ds = tmem + 384;
+  auto t_hi = [&](int c) { return LOCAL ? tmem + 192 * (c & 1) : tmem + 128; };
+  auto t_mid = [&](int c) { return t_hi(c) + 64; };
+  auto t_lo = [&](int c) { return LOCAL ? t_hi(c) + 128 : tmem + 64; };
+  auto sq = [&](int c) { return base + 3 * TILE * (c & 1); };
+  auto sk = [&](int c) { return sq(c) + TILE; };
+  auto sv = [&](int c) { return sq(c) + 2 * TILE; };
   volatile int* dead = &sm.dead;
   auto wait = [&](int i, unsigned ph) { return warp_wait(bar(i), ph, dead); };  // whole warps only
   // the state behind the segment's last chunk is wanted: by the pool, or (LOCAL) by the join
@@ -379,97 +394,107 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 
   if (warp < COMPUTE_WARPS) {
     const int quarter = warp & 3, part = warp >> 2;
-    const int r = quarter * 32 + lane;  // this thread's row of every accumulator and tile: a token, or a v ...
+    const int r = quarter * 32 + lane;  // this thread's row of every accumulator: a token, or a k of the state ...
     const int c0 = 32 * part;           // ... and its 32 columns
     const uint32_t lane_at = (uint32_t)(quarter * 32) << 16;
     // 16-byte chunk i (0..3) of these columns in a 128-byte-swizzled tile of bf16
     auto chunk_at = [&](int i) { return (part >> 1) * BOX + swz128(r, 4 * (part & 1) + i); };
-    float S[32];  // S[v = r][k = c0 ..]
+    auto arrive = [&](int i) {
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar(i));
+    };
+    float S[32];  // S[v = c0 ..][k = r]
     if (resumed) {
+      const long long at = (long long)c0 * D + r;
       if (BF && sg.count == 1) {
-        const uint4* f = reinterpret_cast<const uint4*>(pool) + (r * D + c0) / 8;
+        const uint16_t* f = reinterpret_cast<const uint16_t*>(pool) + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = f[i];
-          S[8 * i] = bf_lo(x.x), S[8 * i + 1] = bf_hi(x.x), S[8 * i + 2] = bf_lo(x.y), S[8 * i + 3] = bf_hi(x.y);
-          S[8 * i + 4] = bf_lo(x.z), S[8 * i + 5] = bf_hi(x.z), S[8 * i + 6] = bf_lo(x.w), S[8 * i + 7] = bf_hi(x.w);
-        }
+        for (int i = 0; i < 32; ++i) S[i] = __uint_as_float((uint32_t)f[i * D] << 16);
       } else {
-        const float4* f = reinterpret_cast<const float4*>(sg.count > 1 ? reinterpret_cast<unsigned char*>(wsp) : pool) +
-                          (r * D + c0) / 4;
+        const float* f = reinterpret_cast<const float*>(sg.count > 1 ? reinterpret_cast<unsigned char*>(wsp) : pool) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 x = f[i];
-          S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
-        }
+        for (int i = 0; i < 32; ++i) S[i] = f[i * D];
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i) S[i] = 0.0f;
     }
-    // S as the bf16 operand of Q S^T: [v][k], 64 k a box
+    // S as the bf16 operand of Q S^T: rows k, 64 v a box
     auto put_state = [&]() {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        sts128(ss + chunk_at(c),
-               make_uint4(pack_bf(S[8 * c], S[8 * c + 1]), pack_bf(S[8 * c + 2], S[8 * c + 3]),
-                          pack_bf(S[8 * c + 4], S[8 * c + 5]), pack_bf(S[8 * c + 6], S[8 * c + 7])));
+      for (int i = 0; i < 4; ++i)
+        sts128(ss + chunk_at(i),
+               make_uint4(pack_bf(S[8 * i], S[8 * i + 1]), pack_bf(S[8 * i + 2], S[8 * i + 3]),
+                          pack_bf(S[8 * i + 4], S[8 * i + 5]), pack_bf(S[8 * i + 6], S[8 * i + 7])));
       fence_async();
     };
-    auto arrive = [&](int i) {
-      __syncwarp();
-      if (lane == 0) bar_arrive(bar(i));
-    };
-    if (!LOCAL) {
-      put_state();
-      arrive(S_IN);
-    }
-    float seg_decay = 0.0f;
-    for (int c = 0; c < chunks; ++c) {
-      const unsigned ph = c & 1;
-      const int n = tokens - c * CHUNK < CHUNK ? tokens - c * CHUNK : CHUNK;  // tokens of this chunk
-      const bool want = want_last || c + 1 < chunks;
-      // K' = hi + mid + lo, token r
-      if (!(ok = wait(DECAY, ph) && wait(FULL_K, ph))) break;
-      const float w = sm.W[r];
-      float total = sm.total;
-      if (want) {
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          const uint32_t at = chunk_at(ch);
-          const uint4 u = lds128(sk + at);
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-          uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // rows behind the sequence's end are somebody else's: not even times zero
-            float f0 = r < n ? bf_lo(x[j]) * w : 0.0f, f1 = r < n ? bf_hi(x[j]) * w : 0.0f;
-            hi[j] = pack_bf(f0, f1);
-            f0 -= bf_lo(hi[j]), f1 -= bf_hi(hi[j]);
-            mid[j] = pack_bf(f0, f1);
-            f0 -= bf_lo(mid[j]), f1 -= bf_hi(mid[j]);
-            lo[j] = pack_bf(f0, f1);
-          }
-          sts128(skp + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          sts128(skp + TILE + at, make_uint4(mid[0], mid[1], mid[2], mid[3]));
-          if (!BF) sts128(skp + 2 * TILE + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
-      }
-      arrive(EMPTY_K);
-      if (n < CHUNK) {  // nor are their values multiplied by the zeros of P and K'
-        if (!(ok = wait(FULL_V, ph))) break;
-        if (r >= n)
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) sts128(sv + chunk_at(ch), make_uint4(0, 0, 0, 0));
-      }
-      fence_async();
-      arrive(KP);
+    auto wanted = [&](int c) { return want_last || c + 1 < chunks; };
+    auto count_of = [&](int c) { return tokens - c * CHUNK < CHUNK ? tokens - c * CHUNK : CHUNK; };
+    uint32_t lo[16];
+    float total = 0.0f;  // of the chunk whose K' was made last
 
-      float eg = 0.0f;
+    // K'^T = hi + mid + lo of chunk c: this thread's k, tokens c0 .. + 31, two a column
+    auto keys = [&](int c) {
+      const int n = count_of(c) - c0;  // of these tokens
+      if (!wait(DECAY_W, c & 1) || !wait(FULL_K + (c & 1), (c >> 1) & 1)) return false;
+      total = sm.total;
+      if (wanted(c)) {
+        const uint32_t row = sk(c) + (r >> 6) * BOX + c0 * 128 + 2 * (r & 7);
+        const uint32_t ch = (r & 63) >> 3;
+        uint32_t hi[16], mid[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 w4 = *reinterpret_cast<const float4*>(sm.W + c0 + j);
+          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+          float f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // rows behind the sequence's end are somebody else's: not even times zero
+            const uint32_t u = lds_u16(row + (j + i) * 128 + ((ch ^ ((j + i) & 7)) << 4));
+            f[i] = j + i < n ? __uint_as_float(u << 16) * w[i] : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int o = j / 2 + i;
+            float f0 = f[2 * i], f1 = f[2 * i + 1];
+            hi[o] = pack_bf(f0, f1);
+            f0 -= bf_lo(hi[o]), f1 -= bf_hi(hi[o]);
+            mid[o] = pack_bf(f0, f1);
+            if (!BF) {
+              f0 -= bf_lo(mid[o]), f1 -= bf_hi(mid[o]);
+              lo[o] = pack_bf(f0, f1);
+            }
+          }
+        }
+        tmem_st(t_hi(c) + lane_at + c0 / 2, hi);
+        tmem_st(t_mid(c) + lane_at + c0 / 2, mid);
+        if (LOCAL) tmem_st(t_lo(c) + lane_at + c0 / 2, lo);
+        tmem_wait_st();
+        tc_before();
+      }
+      arrive(EMPTY_K + (c & 1));
+      if (count_of(c) < CHUNK) {  // nor are their values multiplied by the zeros of P and K'
+        if (!wait(FULL_V + (c & 1), (c >> 1) & 1)) return false;
+        if (r >= count_of(c))
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sts128(sv(c) + chunk_at(i), make_uint4(0, 0, 0, 0));
+        fence_async();
+      }
+      arrive(KP);
+      return true;
+    };
+
+    put_state();
+    arrive(S_IN);
+    float seg_decay = 0.0f;
+    ok = keys(0);
+    for (int c = 0; c < chunks && ok; ++c) {
+      const unsigned ph = c & 1;
+      const bool from_state = resumed || c > 0;
       if (!LOCAL) {
         // the scores' lower triangle, decayed: row i = r
+        if (!(ok = wait(DECAY_G, ph))) break;
         const float gi = sm.G[r];
-        eg = ex2(gi);
         if (!(ok = wait(SCORES, ph))) break;
         tc_after();
         uint32_t pk[16];
@@ -477,133 +502,140 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
           uint32_t x[32];
           tmem_ld(t_sc + lane_at + c0, x);
           tmem_wait_ld(x);
+          const float s0 = ex2(gi - sm.G[c0 + 15]), s1 = ex2(gi - sm.G[c0 + 31]);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int j0 = c0 + 16 * b;
-            float f[16];
-            if (part < quarter) {  // all of the block's tokens are before all of the warp's
-              const float s = ex2(gi - sm.G[j0 + 15]);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(x[16 * b + j]) * (s * sm.E[j0 + j]);
+          for (int j = 0; j < 32; j += 4) {
+            float f[4];
+            if (part < quarter) {  // all of these tokens are before all of the warp's
+              const float4 e = *reinterpret_cast<const float4*>(sm.E + c0 + j);
+              const float s = j < 16 ? s0 : s1;
+              f[0] = e.x * s, f[1] = e.y * s, f[2] = e.z * s, f[3] = e.w * s;
             } else {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                f[j] = j0 + j <= r ? __uint_as_float(x[16 * b + j]) * ex2(gi - sm.G[j0 + j]) : 0.0f;
+              const float4 g = *reinterpret_cast<const float4*>(sm.G + c0 + j);
+              f[0] = ex2(gi - g.x), f[1] = ex2(gi - g.y), f[2] = ex2(gi - g.z), f[3] = ex2(gi - g.w);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) pk[8 * b + j] = pack_bf(f[2 * j], f[2 * j + 1]);
+            for (int i = 0; i < 4; ++i)
+              f[i] = part < quarter || j + i <= lane ? f[i] * __uint_as_float(x[j + i]) : 0.0f;
+            pk[j / 2] = pack_bf(f[0], f[1]);
+            pk[j / 2 + 1] = pack_bf(f[2], f[3]);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = 0u;
         }
-        // P takes the scores' place, once all four warps of these lanes have read theirs
+        // P and lo take the scores' place, once all four warps of these lanes have read theirs
         tc_before();
         arrive(QUARTER + quarter);
         if (!(ok = wait(QUARTER + quarter, ph))) break;
         tc_after();
-        tmem_st(t_sc + lane_at + 16 * part, pk);
+        tmem_st(t_p + lane_at + c0 / 2, pk);
+        if (!BF && wanted(c)) tmem_st(t_lo(c) + lane_at + c0 / 2, lo);
+        if (from_state) {  // Q S^T times e^{G_i}: PV adds to it
+          if (!(ok = wait(FROM_S, ph))) break;
+          tc_after();
+          const float eg = ex2(gi);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t x[16];
+            tmem_ld(t_o + lane_at + c0 + 16 * q, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * eg);
+            tmem_st(t_o + lane_at + c0 + 16 * q, x);
+          }
+        }
         tmem_wait_st();
         tc_before();
         arrive(P_IN);
       }
-
-      if (want) {
+      const float decay = total;
+      if (c + 1 < chunks) {
+        if (!LOCAL && !(ok = wait(HI_DONE, ph))) break;
+        if (!(ok = keys(c + 1))) break;
+      }
+      if (wanted(c)) {
         if (!(ok = wait(DELTA, ph))) break;
         tc_after();
-        seg_decay += total;
-        total = ex2(total);
+        seg_decay += decay;
+        const float d = ex2(decay);
         uint32_t y[32];
         tmem_ld(t_ds + lane_at + c0, y);
         tmem_wait_ld(y);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[i] = fmaf(total, S[i], __uint_as_float(y[i]));
+        for (int i = 0; i < 32; ++i) S[i] = fmaf(d, S[i], __uint_as_float(y[i]));
         if (!LOCAL && c + 1 < chunks) put_state();
+        tc_before();
       }
-      tc_before();
-      if (!LOCAL) arrive(S_IN);
-
+      arrive(S_IN);
       if (!LOCAL) {
+        const int n = count_of(c);
         if (!(ok = wait(OUT, ph))) break;
         tc_after();
-        const bool from_state = resumed || c > 0;
-        eg *= a.scale;
-        // by way of shared memory (this warp's own part of K', which nobody reads now), so that
-        // the stores are rows' 64 bytes together
+        // by way of shared memory (this warp's own part of Q, which nobody reads any more), so
+        // that the stores are rows' 64 bytes together
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t y[16], z[16];
-          tmem_ld(t_op + lane_at + c0 + 16 * q, y);
-          if (from_state) {
-            tmem_ld(t_os + lane_at + c0 + 16 * q, z);
-            tmem_wait_ld(y, z);
-          } else {
-            tmem_wait_ld(y);
-          }
+          uint32_t y[16];
+          tmem_ld(t_o + lane_at + c0 + 16 * q, y);
+          tmem_wait_ld(y);
           uint32_t w[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float f0 = a.scale * __uint_as_float(y[2 * j]), f1 = a.scale * __uint_as_float(y[2 * j + 1]);
-            if (from_state) {
-              f0 = fmaf(eg, __uint_as_float(z[2 * j]), f0);
-              f1 = fmaf(eg, __uint_as_float(z[2 * j + 1]), f1);
-            }
-            w[j] = pack_bf(f0, f1);
-          }
-          sts128(skp + chunk_at(2 * q), make_uint4(w[0], w[1], w[2], w[3]));
-          sts128(skp + chunk_at(2 * q + 1), make_uint4(w[4], w[5], w[6], w[7]));
+          for (int j = 0; j < 8; ++j)
+            w[j] = pack_bf(a.scale * __uint_as_float(y[2 * j]), a.scale * __uint_as_float(y[2 * j + 1]));
+          sts128(sq(c) + chunk_at(2 * q), make_uint4(w[0], w[1], w[2], w[3]));
+          sts128(sq(c) + chunk_at(2 * q + 1), make_uint4(w[4], w[5], w[6], w[7]));
         }
-        __syncwarp();
+        tc_before();
+        arrive(O_READ);
         __nv_bfloat16* o = a.out + (row0 + (long long)c * CHUNK + quarter * 32) * a.ldo + h * D + c0 + 8 * (lane & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 8 * i + (lane >> 2);
-          const uint4 u = lds128(skp + (part >> 1) * BOX + swz128(quarter * 32 + t, 4 * (part & 1) + (lane & 3)));
+          const uint4 u = lds128(sq(c) + (part >> 1) * BOX + swz128(quarter * 32 + t, 4 * (part & 1) + (lane & 3)));
           if (quarter * 32 + t < n) *reinterpret_cast<uint4*>(o + t * a.ldo) = u;
         }
-        __syncwarp();  // before K' goes there again
-        tc_before();
-        arrive(O_READ);
+        fence_async();  // before the copy of a later Q
+        arrive(EMPTY_Q + (c & 1));
       }
     }
     if (ok && want_last) {
+      const long long at = (long long)c0 * D + r;
       if (BF) {
-        uint4* f = reinterpret_cast<uint4*>(pool) + (r * D + c0) / 8;
+        __nv_bfloat16* f = reinterpret_cast<__nv_bfloat16*>(pool) + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          f[i] = make_uint4(pack_bf(S[8 * i], S[8 * i + 1]), pack_bf(S[8 * i + 2], S[8 * i + 3]),
-                            pack_bf(S[8 * i + 4], S[8 * i + 5]), pack_bf(S[8 * i + 6], S[8 * i + 7]));
+        for (int i = 0; i < 32; ++i) f[i * D] = __float2bfloat16_rn(S[i]);
       } else {
-        float4* f = reinterpret_cast<float4*>(LOCAL ? reinterpret_cast<unsigned char*>(wsp) : pool) + (r * D + c0) / 4;
+        float* f = reinterpret_cast<float*>(LOCAL ? reinterpret_cast<unsigned char*>(wsp) : pool) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        for (int i = 0; i < 32; ++i) f[i * D] = S[i];
         if (LOCAL && threadIdx.x == 0) p.decays[number * a.heads + h] = seg_decay;
       }
     }
   } else if (warp == COMPUTE_WARPS) {  // copies, and the decays (four tokens a lane)
     for (int c = 0; c < chunks; ++c) {
-      const unsigned prev = (c & 1) ^ 1;  // the phase of chunk c - 1
       const int row = (int)(row0 + (long long)c * CHUNK);
-      auto load = [&](int full, int empty, uint32_t dst, const CUtensorMap* map, int col) {
-        if (c > 0 && !(ok = wait(empty, prev))) return;
-        if (lane == 0) {
-          bar_expect(bar(full), TILE);
-          tma_load(dst, map, col, row, bar(full));
-          tma_load(dst + BOX, map, col + 64, row, bar(full));
-        }
-        __syncwarp();
-      };
-      load(FULL_K, EMPTY_K, sk, &tk, hk * D);
-      if (!LOCAL && ok) load(FULL_Q, EMPTY_Q, sq, &tq, hk * D);
-      if (!ok) break;
       const long long t0 = row0 + (long long)c * CHUNK + 4 * lane;
       const int n = tokens - c * CHUNK;
       float g[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = 4 * lane + j < n ? a.g[(t0 + j) * a.ldg + h] : 0.0f;
-        g[j] = (x < G_MIN ? G_MIN : x) * LOG2E;
-      }
+      for (int j = 0; j < 4; ++j) g[j] = 4 * lane + j < n ? a.g[(t0 + j) * a.ldg + h] : 0.0f;
+      auto load = [&](int full, int empty, uint32_t dst, const CUtensorMap* map, int col) {
+        if (c > 1 && !(ok = wait(empty + (c & 1), ((c >> 1) & 1) ^ 1))) return;  // its reader two chunks ago
+        if (lane == 0) {
+          const uint32_t b = bar(full + (c & 1));
+          bar_expect(b, TILE);
+          tma_load(dst, map, col, row, b);
+          tma_load(dst + BOX, map, col + 64, row, b);
+        }
+        __syncwarp();
+      };
+      load(FULL_K, EMPTY_K, sk(c), &tk, hk * D);
+      if (ok) load(FULL_V, EMPTY_V, sv(c), &tv, h * D);
+      if (!LOCAL && ok) load(FULL_Q, EMPTY_Q, sq(c), &tq, hk * D);
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = (g[j] < G_MIN ? G_MIN : g[j]) * LOG2E;
       float pre[4], suf[4];  // sums up to and behind each token, each from its own end: the near ones exact
       pre[0] = g[0], pre[1] = pre[0] + g[1], pre[2] = pre[1] + g[2], pre[3] = pre[2] + g[3];
       suf[3] = 0.0f, suf[2] = g[3], suf[1] = suf[2] + g[2], suf[0] = suf[1] + g[1];
@@ -621,77 +653,83 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) pre[j] += before, suf[j] += behind;
       const float ref = __shfl_sync(0xffffffffu, pre[3], lane | 3);
-      // the arrays' readers are done with the chunk before
-      if (c > 0 && !(ok = wait(LOCAL ? KP : P_IN, prev))) break;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sm.G[4 * lane + j] = pre[j];
-        sm.W[4 * lane + j] = ex2(suf[j]);
-        sm.E[4 * lane + j] = ex2(ref - pre[j]);
-      }
+      const unsigned prev = (c & 1) ^ 1;  // the phase of chunk c - 1, whose readers have to be done
+      if (c > 0 && !(ok = wait(KP, prev))) break;
+      *reinterpret_cast<float4*>(sm.W + 4 * lane) = make_float4(ex2(suf[0]), ex2(suf[1]), ex2(suf[2]), ex2(suf[3]));
       if (lane == 0) sm.total = total;
       __syncwarp();
-      if (lane == 0) bar_arrive(bar(DECAY));
-      // (the last of a chunk's operands to come free)
-      load(FULL_V, EMPTY_V, sv, &tv, h * D);
-      if (!ok) break;
+      if (lane == 0) bar_arrive(bar(DECAY_W));
+      if (!LOCAL) {
+        if (c > 0 && !(ok = wait(P_IN, prev))) break;
+        *reinterpret_cast<float4*>(sm.G + 4 * lane) = make_float4(pre[0], pre[1], pre[2], pre[3]);
+        *reinterpret_cast<float4*>(sm.E + 4 * lane) =
+            make_float4(ex2(ref - pre[0]), ex2(ref - pre[1]), ex2(ref - pre[2]), ex2(ref - pre[3]));
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar(DECAY_G));
+      }
     }
   } else {  // matrix products
+    constexpr uint32_t id_kk = idesc_bf16(128, 128, false, false), id_kmn = idesc_bf16(128, 128, false, true);
     for (int c = 0; c < chunks; ++c) {
-      const unsigned ph = c & 1;
-      const bool want = want_last || c + 1 < chunks;
+      const unsigned ph = c & 1, ph2 = (c >> 1) & 1;
+      const bool want = want_last || c + 1 < chunks, from_state = resumed || c > 0;
+      // K'^T's parts times V
+      auto delta = [&](uint32_t keys, bool first) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_ts(t_ds, keys + 8 * k, desc_mn(sv(c) + 2048 * k, BOX), id_kmn, !first || k > 0);
+      };
       if (!LOCAL) {
-        if (!(ok = wait(FULL_Q, ph) && wait(FULL_K, ph))) break;
+        if (!(ok = wait(FULL_Q + ph, ph2) && wait(FULL_K + ph, ph2))) break;
         tc_after();
         if (lane == 0) {
-          constexpr uint32_t id = idesc_bf16(128, 128, false, false);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint32_t at = (k >> 2) * BOX + 32 * (k & 3);
-            mma_ss(t_sc, desc_k(sq + at), desc_k(sk + at), id, k > 0);
+            mma_ss(t_sc, desc_k(sq(c) + at), desc_k(sk(c) + at), id_kk, k > 0);
           }
           mma_commit(bar(SCORES));
-          mma_commit(bar(EMPTY_K));
-        }
-        __syncwarp();
-        const bool from_state = resumed || c > 0;
-        if (!(ok = wait(S_IN, ph) && (c == 0 || wait(O_READ, ph ^ 1)))) break;
-        tc_after();
-        if (lane == 0) {
-          if (from_state) {
-            constexpr uint32_t id = idesc_bf16(128, 128, false, false);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t at = (k >> 2) * BOX + 32 * (k & 3);
-              mma_ss(t_os, desc_k(sq + at), desc_k(ss + at), id, k > 0);
-            }
-          }
-          mma_commit(bar(EMPTY_Q));
+          mma_commit(bar(EMPTY_K + ph));
         }
         __syncwarp();
       }
-      if (!(ok = wait(KP, ph) && wait(FULL_V, ph))) break;
+      // (S_IN: the threads have read the chunk before's K'^T V, too)
+      if (!(ok = wait(S_IN, ph) && (LOCAL || c == 0 || wait(O_READ, ph ^ 1)))) break;
       tc_after();
-      if (lane == 0 && want) {
-        constexpr uint32_t id = idesc_bf16(128, 128, true, true);
-#pragma unroll
-        for (int part = BF ? 1 : 2; part >= 0; --part)
+      if (!LOCAL && lane == 0) {
+        if (from_state) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_ss(t_ds, desc_mn(sv + 2048 * k, BOX), desc_mn(skp + part * TILE + 2048 * k, BOX), id,
-                   part < (BF ? 1 : 2) || k > 0);
-        if (LOCAL) mma_commit(bar(EMPTY_V));
-        mma_commit(bar(DELTA));
+            mma_ss(t_o, desc_k(sq(c) + (k >> 2) * BOX + 32 * (k & 3)), desc_mn(ss + 2048 * k, BOX), id_kmn, k > 0);
+        }
+        mma_commit(bar(FROM_S));  // (every chunk: its phases count them)
+      }
+      __syncwarp();
+      if (!(ok = wait(KP, ph) && wait(FULL_V + ph, ph2))) break;
+      tc_after();
+      if (lane == 0 && want) {
+        if (LOCAL) delta(t_lo(c), true);  // smallest first
+        delta(t_mid(c), !LOCAL);
+        delta(t_hi(c), false);
+        if (LOCAL) {
+          mma_commit(bar(EMPTY_V + ph));
+          mma_commit(bar(DELTA));
+        } else {
+          mma_commit(bar(HI_DONE));
+        }
       }
       __syncwarp();
       if (!LOCAL) {
         if (!(ok = wait(P_IN, ph))) break;
         tc_after();
         if (lane == 0) {
-          constexpr uint32_t id = idesc_bf16(128, 128, false, true);
+          if (want) {
+            if (!BF) delta(t_lo(c), false);
+            mma_commit(bar(DELTA));
+          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_ts(t_op, t_sc + 8 * k, desc_mn(sv + 2048 * k, BOX), id, k > 0);
-          mma_commit(bar(EMPTY_V));
+          for (int k = 0; k < 8; ++k)
+            mma_ts(t_o, t_p + 8 * k, desc_mn(sv(c) + 2048 * k, BOX), id_kmn, from_state || k > 0);
+          mma_commit(bar(EMPTY_V + ph));
           mma_commit(bar(OUT));
         }
         __syncwarp();
