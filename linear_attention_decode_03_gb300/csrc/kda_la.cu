@@ -262,6 +262,12 @@ __device__ bool find_segment(const LaArgs& a, int m, long long limit, long long 
   return false;
 }
 
+// the upper 16 bits of two floats, and a float without its lower 16: bf16 parts cut off, not rounded
+__device__ __forceinline__ uint32_t top_halves(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float bf_cut(float x) { return bf_hi(__float_as_uint(x)); }
+
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -300,7 +306,8 @@ static_assert(sizeof(ChunkMisc) <= MISC, "misc area");
 template <bool BF, bool LOCAL>
 __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     la_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                    const __grid_constant__ CUtensorMap tv, const ChunkArgs p) {
+                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                    const ChunkArgs p) {
   const LaArgs& a = p.a;
   extern __shared__ __align__(1024) unsigned char dyn[];
   // (all shared memory is dynamic: the seven operand tiles leave no room for a second alignment)
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
                        : i >= EMPTY_Q                     ? COMPUTE_WARPS
                                                           : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (!LOCAL) prefetch_map(&tq);
+    if (!LOCAL) prefetch_map(&tq), prefetch_map(&to);
     prefetch_map(&tk);
     prefetch_map(&tv);
   }
@@ -430,45 +437,55 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     };
     auto wanted = [&](int c) { return want_last || c + 1 < chunks; };
     auto count_of = [&](int c) { return tokens - c * CHUNK < CHUNK ? tokens - c * CHUNK : CHUNK; };
-    uint32_t lo[16];
+    uint32_t lo[2][8];
     float total = 0.0f;  // of the chunk whose K' was made last
 
-    // K'^T = hi + mid + lo of chunk c: this thread's k, tokens c0 .. + 31, two a column
+    // K'^T = hi + mid + lo of chunk c: k quarter * 32 .. + 31, tokens c0 .. + 31, two a column.  The
+    // transpose is ldmatrix's, whose fragments are what tensor memory takes in 16 x 128-bit form:
+    // thread l has k = l / 4 + 8 i, tokens 2 (l % 4), + 1 (+ 8 g).  Cutting bits off (not rounding)
+    // gives three parts of 8 bits that add up to all 24.
     auto keys = [&](int c) {
-      const int n = count_of(c) - c0;  // of these tokens
+      const int n = count_of(c) - c0 - 2 * (lane & 3);  // the thread's first token is in its chunk if > 0, ...
       if (!wait(DECAY_W, c & 1) || !wait(FULL_K + (c & 1), (c >> 1) & 1)) return false;
       total = sm.total;
       if (wanted(c)) {
-        const uint32_t row = sk(c) + (r >> 6) * BOX + c0 * 128 + 2 * (r & 7);
-        const uint32_t ch = (r & 63) >> 3;
-        uint32_t hi[16], mid[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 w4 = *reinterpret_cast<const float4*>(sm.W + c0 + j);
-          const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-          float f[4];
+        for (int half = 0; half < 2; ++half) {  // 16 k
+          uint32_t hi[8], mid[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // rows behind the sequence's end are somebody else's: not even times zero
-            const uint32_t u = lds_u16(row + (j + i) * 128 + ((ch ^ ((j + i) & 7)) << 4));
-            f[i] = j + i < n ? __uint_as_float(u << 16) * w[i] : 0.0f;
-          }
+          for (int g2 = 0; g2 < 4; g2 += 2) {  // 16 tokens
+            uint32_t u[4];
+            const int j = c0 + 8 * (g2 + (lane >> 4)) + (lane & 7);
+            const int k8 = quarter * 4 + half * 2 + ((lane >> 3) & 1);  // 8 k: a 16-byte chunk
+            ldsm_x4_trans(u, sk(c) + (k8 >> 3) * BOX + swz128(j, k8 & 7));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int o = j / 2 + i;
-            float f0 = f[2 * i], f1 = f[2 * i + 1];
-            hi[o] = pack_bf(f0, f1);
-            f0 -= bf_lo(hi[o]), f1 -= bf_hi(hi[o]);
-            mid[o] = pack_bf(f0, f1);
-            if (!BF) {
-              f0 -= bf_lo(mid[o]), f1 -= bf_hi(mid[o]);
-              lo[o] = pack_bf(f0, f1);
+            for (int e = 0; e < 2; ++e) {
+              const int g = g2 + e;
+              const float2 w = *reinterpret_cast<const float2*>(sm.W + c0 + 8 * g + 2 * (lane & 3));
+              // rows behind the sequence's end are somebody else's: not even times zero
+              const uint32_t live = n > 8 * g + 1 ? 0xffffffffu : n > 8 * g ? 0xffffu : 0u;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int o = 2 * g + i;
+                const uint32_t x = u[2 * e + i] & live;
+                float f0 = bf_lo(x) * w.x, f1 = bf_hi(x) * w.y;
+                hi[o] = top_halves(f0, f1);
+                f0 -= bf_cut(f0), f1 -= bf_cut(f1);
+                if (BF) {
+                  mid[o] = pack_bf(f0, f1);
+                } else {
+                  mid[o] = top_halves(f0, f1);
+                  f0 -= bf_cut(f0), f1 -= bf_cut(f1);
+                  lo[half][o] = top_halves(f0, f1);
+                }
+              }
             }
           }
+          const uint32_t at = lane_at + ((uint32_t)(16 * half) << 16) + c0 / 2;
+          tmem_st_frag(t_hi(c) + at, hi);
+          tmem_st_frag(t_mid(c) + at, mid);
+          if (LOCAL) tmem_st_frag(t_lo(c) + at, lo[half]);
         }
-        tmem_st(t_hi(c) + lane_at + c0 / 2, hi);
-        tmem_st(t_mid(c) + lane_at + c0 / 2, mid);
-        if (LOCAL) tmem_st(t_lo(c) + lane_at + c0 / 2, lo);
         tmem_wait_st();
         tc_before();
       }
@@ -499,26 +516,29 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         tc_after();
         uint32_t pk[16];
         if (part <= quarter) {
-          uint32_t x[32];
-          tmem_ld(t_sc + lane_at + c0, x);
-          tmem_wait_ld(x);
-          const float s0 = ex2(gi - sm.G[c0 + 15]), s1 = ex2(gi - sm.G[c0 + 31]);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float f[4];
-            if (part < quarter) {  // all of these tokens are before all of the warp's
-              const float4 e = *reinterpret_cast<const float4*>(sm.E + c0 + j);
-              const float s = j < 16 ? s0 : s1;
-              f[0] = e.x * s, f[1] = e.y * s, f[2] = e.z * s, f[3] = e.w * s;
-            } else {
-              const float4 g = *reinterpret_cast<const float4*>(sm.G + c0 + j);
-              f[0] = ex2(gi - g.x), f[1] = ex2(gi - g.y), f[2] = ex2(gi - g.z), f[3] = ex2(gi - g.w);
+          for (int q = 0; q < 2; ++q) {
+            const int j0 = c0 + 16 * q;
+            uint32_t x[16];
+            tmem_ld(t_sc + lane_at + j0, x);
+            tmem_wait_ld(x);
+            const float s = ex2(gi - sm.G[j0 + 15]);
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              float f[4];
+              if (part < quarter) {  // all of these tokens are before all of the warp's
+                const float4 e = *reinterpret_cast<const float4*>(sm.E + j0 + j);
+                f[0] = e.x * s, f[1] = e.y * s, f[2] = e.z * s, f[3] = e.w * s;
+              } else {
+                const float4 g = *reinterpret_cast<const float4*>(sm.G + j0 + j);
+                f[0] = ex2(gi - g.x), f[1] = ex2(gi - g.y), f[2] = ex2(gi - g.z), f[3] = ex2(gi - g.w);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                f[i] = part < quarter || 16 * q + j + i <= lane ? f[i] * __uint_as_float(x[j + i]) : 0.0f;
+              pk[8 * q + j / 2] = pack_bf(f[0], f[1]);
+              pk[8 * q + j / 2 + 1] = pack_bf(f[2], f[3]);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              f[i] = part < quarter || j + i <= lane ? f[i] * __uint_as_float(x[j + i]) : 0.0f;
-            pk[j / 2] = pack_bf(f[0], f[1]);
-            pk[j / 2 + 1] = pack_bf(f[2], f[3]);
           }
         } else {
 #pragma unroll
@@ -530,7 +550,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         if (!(ok = wait(QUARTER + quarter, ph))) break;
         tc_after();
         tmem_st(t_p + lane_at + c0 / 2, pk);
-        if (!BF && wanted(c)) tmem_st(t_lo(c) + lane_at + c0 / 2, lo);
+        if (!BF && wanted(c)) {
+          tmem_st_frag(t_lo(c) + lane_at + c0 / 2, lo[0]);
+          tmem_st_frag(t_lo(c) + lane_at + (16u << 16) + c0 / 2, lo[1]);
+        }
         if (from_state) {  // Q S^T times e^{G_i}: PV adds to it
           if (!(ok = wait(FROM_S, ph))) break;
           tc_after();
@@ -548,6 +571,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         tmem_wait_st();
         tc_before();
         arrive(P_IN);
+        if (c > 0) {  // the chunk before's outputs have left its Q
+          if (lane == 0) tma_store_read();
+          arrive(EMPTY_Q + (ph ^ 1));
+        }
       }
       const float decay = total;
       if (c + 1 < chunks) {
@@ -572,8 +599,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         const int n = count_of(c);
         if (!(ok = wait(OUT, ph))) break;
         tc_after();
-        // by way of shared memory (this warp's own part of Q, which nobody reads any more), so
-        // that the stores are rows' 64 bytes together
+        // by way of shared memory, 2 KB of Q (which nobody reads any more) a warp: rows of 64 bytes,
+        // 64-byte swizzle (16-byte chunk i of row r at i ^ (r / 2) % 4), sent as one box if all 32 are the sequence's
+        const uint32_t stage = sq(c) + warp * 2048;
+        auto at64 = [&](int row, int i) { return stage + row * 64 + ((i ^ ((row >> 1) & 3)) << 4); };
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t y[16];
@@ -583,22 +612,28 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             w[j] = pack_bf(a.scale * __uint_as_float(y[2 * j]), a.scale * __uint_as_float(y[2 * j + 1]));
-          sts128(sq(c) + chunk_at(2 * q), make_uint4(w[0], w[1], w[2], w[3]));
-          sts128(sq(c) + chunk_at(2 * q + 1), make_uint4(w[4], w[5], w[6], w[7]));
+          sts128(at64(lane, 2 * q), make_uint4(w[0], w[1], w[2], w[3]));
+          sts128(at64(lane, 2 * q + 1), make_uint4(w[4], w[5], w[6], w[7]));
         }
         tc_before();
         arrive(O_READ);
-        __nv_bfloat16* o = a.out + (row0 + (long long)c * CHUNK + quarter * 32) * a.ldo + h * D + c0 + 8 * (lane & 3);
+        const long long row = row0 + (long long)c * CHUNK + quarter * 32;
+        fence_async();
+        __syncwarp();
+        if (n >= quarter * 32 + 32) {
+          if (lane == 0) tma_store(&to, h * D + c0, (int)row, stage);
+        } else {
+          __nv_bfloat16* o = a.out + row * a.ldo + h * D + c0 + 8 * (lane & 3);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 8 * i + (lane >> 2);
-          const uint4 u = lds128(sq(c) + (part >> 1) * BOX + swz128(quarter * 32 + t, 4 * (part & 1) + (lane & 3)));
-          if (quarter * 32 + t < n) *reinterpret_cast<uint4*>(o + t * a.ldo) = u;
+          for (int i = 0; i < 4; ++i) {
+            const int t = 8 * i + (lane >> 2);
+            const uint4 u = lds128(at64(t, lane & 3));
+            if (quarter * 32 + t < n) *reinterpret_cast<uint4*>(o + t * a.ldo) = u;
+          }
         }
-        fence_async();  // before the copy of a later Q
-        arrive(EMPTY_Q + (c & 1));
       }
     }
+    if (!LOCAL && lane == 0) tma_store_read();  // before the memory goes
     if (ok && want_last) {
       const long long at = (long long)c0 * D + r;
       if (BF) {
@@ -632,7 +667,6 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       };
       load(FULL_K, EMPTY_K, sk(c), &tk, hk * D);
       if (ok) load(FULL_V, EMPTY_V, sv(c), &tv, h * D);
-      if (!LOCAL && ok) load(FULL_Q, EMPTY_Q, sq(c), &tq, hk * D);
       if (!ok) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) g[j] = (g[j] < G_MIN ? G_MIN : g[j]) * LOG2E;
@@ -660,6 +694,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar(DECAY_W));
       if (!LOCAL) {
+        load(FULL_Q, EMPTY_Q, sq(c), &tq, hk * D);  // (the last of the three to come free)
+        if (!ok) break;
         if (c > 0 && !(ok = wait(P_IN, prev))) break;
         *reinterpret_cast<float4*>(sm.G + 4 * lane) = make_float4(pre[0], pre[1], pre[2], pre[3]);
         *reinterpret_cast<float4*>(sm.E + 4 * lane) =
@@ -923,8 +959,8 @@ bool la_sizes_ok(long long rows, int heads, long long seqs, long long max_len) {
 }
 
 template <bool BF>
-int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& p,
-                      const Cut& cut, cudaStream_t st) {
+int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
+                      const ChunkArgs& p, const Cut& cut, cudaStream_t st) {
   const unsigned grid = (unsigned)(cut.segments * p.a.heads);
   // the shared-memory attribute is per device and cheap: set on every call
   if (cudaFuncSetAttribute(la_chunk_kernel<BF, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
@@ -935,10 +971,10 @@ int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
     if (cudaFuncSetAttribute(la_chunk_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
         cudaSuccess)
       return KDA_ECUDA;
-    la_chunk_kernel<false, true><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, p);
+    la_chunk_kernel<false, true><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, to, p);
     la_join_kernel<BF><<<(unsigned)(p.a.seqs * p.a.heads * 4), 256, 0, st>>>(p);
   }
-  la_chunk_kernel<BF, false><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, p);
+  la_chunk_kernel<BF, false><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, to, p);
   return launched();
 }
 
@@ -976,14 +1012,15 @@ extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long 
   const Cut cut = la_cut(rows, heads, seqs, max_len, sms);
   const long long need = cut.split ? (cut.segments * heads * (D * D + 1) * 4 + 15) / 16 * 16 : 0;
   if (need > 0 && (!workspace || workspace_bytes < need || !ptr_aligned(workspace, 16))) return KDA_EINVAL;
-  CUtensorMap tq = {}, tk = {}, tv = {};
+  CUtensorMap tq = {}, tk = {}, tv = {}, to = {};
   if (rows > 0) {
-    if (!on_device(q, dev) || !on_device(k, dev) || !on_device(v, dev)) return KDA_EINVAL;
+    if (!on_device(q, dev) || !on_device(k, dev) || !on_device(v, dev) || !on_device(out, dev)) return KDA_EINVAL;
     const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUtensorMapSwizzle s = CU_TENSOR_MAP_SWIZZLE_128B;
     if (!encode_2d(&tq, t, q, rows, (long long)qk_heads * D, ldq * 2, 64, CHUNK, s) ||
         !encode_2d(&tk, t, k, rows, (long long)qk_heads * D, ldk * 2, 64, CHUNK, s) ||
-        !encode_2d(&tv, t, v, rows, (long long)heads * D, ldv * 2, 64, CHUNK, s))
+        !encode_2d(&tv, t, v, rows, (long long)heads * D, ldv * 2, 64, CHUNK, s) ||
+        !encode_2d(&to, t, out, rows, (long long)heads * D, ldo * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return KDA_ECUDA;
   }
   ChunkArgs p;
@@ -994,8 +1031,8 @@ extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long 
   p.m = cut.m;
   p.segments = cut.segments;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  return state_dtype == KDA_STATE_BF16 ? la_prefill_launch<true>(tq, tk, tv, p, cut, st)
-                                       : la_prefill_launch<false>(tq, tk, tv, p, cut, st);
+  return state_dtype == KDA_STATE_BF16 ? la_prefill_launch<true>(tq, tk, tv, to, p, cut, st)
+                                       : la_prefill_launch<false>(tq, tk, tv, to, p, cut, st);
 }
 
 extern "C" int kda_la_check(void* cuda_stream, unsigned* device_flags) {
