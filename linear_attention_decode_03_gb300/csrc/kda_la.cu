@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
+  if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // tensor memory: scores, then P and lo; hi and mid; outputs; K'^T V.  (LOCAL: two sets of hi, mid, lo; K'^T V)
   const uint32_t t_sc = tmem, t_p = tmem, t_o = tmem + 256, t_ds = tmem + 384;
   auto t_hi = [&](int c) { return LOCAL ? tmem + 192 * (c & 1) : tmem + 128; };
@@ -410,6 +411,9 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar(i));
     };
+    // As a dependent launch all of the above and the first copies overlap the join; the state the segment
+    // starts from is its result.  (By itself the wait is a no-op.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float S[32];  // S[v = c0 ..][k = r]
     if (resumed) {
       const long long at = (long long)c0 * D + r;
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       } else {
         const float* f = reinterpret_cast<const float*>(sg.count > 1 ? reinterpret_cast<unsigned char*>(wsp) : pool) + at;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[i] = f[i * D];
+        for (int i = 0; i < 32; ++i) S[i] = __ldcg(f + i * D);
       }
     } else {
 #pragma unroll
@@ -794,15 +798,18 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   if (warp == COMPUTE_WARPS + 1) tmem_free(tmem, 512);
 }
 
-// From the segments' own states to the states they start from, elementwise: 1/4 of
-// a state a CTA, in place in the workspace.
+// From the segments' own states to the states they start from, elementwise and in place in
+// the workspace: four values a thread, JOIN_PARTS CTAs a state, the loads of JOIN_AHEAD segments
+// in flight together.
+constexpr int JOIN_PARTS = 16, JOIN_AHEAD = 8;
 template <bool BF>
 __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
   const LaArgs& a = p.a;
   __shared__ Segment s_seg;
   __shared__ long long s_number;
   __shared__ int s_found;
-  const long long task = blockIdx.x / 4;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long task = blockIdx.x / JOIN_PARTS;
   const long long seq = task / a.heads;
   const int h = (int)(task % a.heads);
   {
@@ -820,38 +827,36 @@ __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
   const int slot = a.slots[seq];
   if (slot < 0 || slot >= a.pool) return;
   const int count = s_seg.count;
-  const long long at = (long long)(blockIdx.x % 4) * (D * D / 4) + 4 * threadIdx.x;  // + 1024 i
-  const bool has = a.has_state && a.has_state[seq];
-  float4 S[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long e = ((long long)slot * a.heads + h) * (D * D) + at + 1024 * i;
-    S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (has && BF) {
+  const int at = (int)(blockIdx.x % JOIN_PARTS) * (D * D / JOIN_PARTS) + 4 * threadIdx.x;
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.has_state && a.has_state[seq]) {
+    const long long e = ((long long)slot * a.heads + h) * (D * D) + at;
+    if (BF) {
       const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.state) + e);
-      S[i] = make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
-    } else if (has) {
-      S[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(a.state) + e);
+      S = make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
+    } else {
+      S = *reinterpret_cast<const float4*>(static_cast<const float*>(a.state) + e);
     }
   }
-  const long long step = (long long)a.heads * D * D;
+  const long long step = (long long)a.heads * (D * D / 4);
   float4* w = reinterpret_cast<float4*>(p.ws + (s_number * a.heads + h) * (D * D) + at);
   const float* d = p.decays + s_number * a.heads + h;
-  for (int s = 0; s < count; ++s, w += step / 4, d += a.heads) {
-    const bool more = s + 1 < count;
-    float4 own[4];
-    float f = 0.0f;
-    if (more) {
-      f = ex2(*d);
+  // the segments' states are the kernel before's
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int s0 = 0; s0 < count; s0 += JOIN_AHEAD, w += JOIN_AHEAD * step, d += (long long)JOIN_AHEAD * a.heads) {
+    float4 own[JOIN_AHEAD];
+    float f[JOIN_AHEAD];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) own[i] = w[256 * i];
+    for (int i = 0; i < JOIN_AHEAD; ++i) {  // (the last segment's own state is nobody's start)
+      const bool more = s0 + i + 1 < count;
+      own[i] = more ? __ldcg(w + i * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+      f[i] = more ? __ldcg(d + (long long)i * a.heads) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[256 * i] = S[i];
-      if (more)
-        S[i] = make_float4(fmaf(f, S[i].x, own[i].x), fmaf(f, S[i].y, own[i].y), fmaf(f, S[i].z, own[i].z),
-                           fmaf(f, S[i].w, own[i].w));
+    for (int i = 0; i < JOIN_AHEAD; ++i) {
+      if (s0 + i < count) w[i * step] = S;
+      const float e = ex2(f[i]);
+      S = make_float4(fmaf(e, S.x, own[i].x), fmaf(e, S.y, own[i].y), fmaf(e, S.z, own[i].z), fmaf(e, S.w, own[i].w));
     }
   }
 }
@@ -961,7 +966,11 @@ bool la_sizes_ok(long long rows, int heads, long long seqs, long long max_len) {
 template <bool BF>
 int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                       const ChunkArgs& p, const Cut& cut, cudaStream_t st) {
-  const unsigned grid = (unsigned)(cut.segments * p.a.heads);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cut.segments * p.a.heads), 1, 1);
+  cfg.blockDim = dim3(CHUNK_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = CHUNK_SMEM;
+  cfg.stream = st;
   // the shared-memory attribute is per device and cheap: set on every call
   if (cudaFuncSetAttribute(la_chunk_kernel<BF, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
       cudaSuccess)
@@ -969,12 +978,25 @@ int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   if (cut.split) {
     // (the workspace is fp32 whatever the pool)
     if (cudaFuncSetAttribute(la_chunk_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
-        cudaSuccess)
+            cudaSuccess ||
+        cudaLaunchKernelEx(&cfg, la_chunk_kernel<false, true>, tq, tk, tv, to, p) != cudaSuccess)
       return KDA_ECUDA;
-    la_chunk_kernel<false, true><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, to, p);
-    la_join_kernel<BF><<<(unsigned)(p.a.seqs * p.a.heads * 4), 256, 0, st>>>(p);
+    // the two kernels behind it may start while the one before ends, and wait where they read its results
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchConfig_t join = cfg;
+    join.gridDim = dim3((unsigned)(p.a.seqs * p.a.heads * JOIN_PARTS), 1, 1);
+    join.blockDim = dim3(256, 1, 1);
+    join.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&join, la_join_kernel<BF>, p) != cudaSuccess ||
+        cudaLaunchKernelEx(&cfg, la_chunk_kernel<BF, false>, tq, tk, tv, to, p) != cudaSuccess)
+      return KDA_ECUDA;
+  } else if (cudaLaunchKernelEx(&cfg, la_chunk_kernel<BF, false>, tq, tk, tv, to, p) != cudaSuccess) {
+    return KDA_ECUDA;
   }
-  la_chunk_kernel<BF, false><<<grid, CHUNK_THREADS, CHUNK_SMEM, st>>>(tq, tk, tv, to, p);
   return launched();
 }
 
@@ -1003,8 +1025,8 @@ extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long 
                   out, ldo) ||
       !cu_seqlens || !ptr_aligned(cu_seqlens, 4) || !ptr_aligned(has_state, 4))
     return KDA_EINVAL;
-  // the largest grids: a CTA a segment and head, four a sequence and head
-  if ((rows / CHUNK + seqs) > 0x7fffffffLL / heads || seqs > 0x7fffffffLL / 4 / heads) return KDA_EINVAL;
+  // the largest grids: a CTA a segment and head, JOIN_PARTS a sequence and head
+  if ((rows / CHUNK + seqs) > 0x7fffffffLL / heads || seqs > 0x7fffffffLL / JOIN_PARTS / heads) return KDA_EINVAL;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ECUDA;
   const int sms = sm_count(dev);
