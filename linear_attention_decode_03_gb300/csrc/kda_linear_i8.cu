@@ -2,59 +2,417 @@
 // (sm_103a): y[m, n] = sx[m] sw[n] sum_k x[m, k] W[n, k], int8 in, bf16 out
 // (see include/kda_ops.h, kda_linear_i8).
 //
-// A 64 x 64 output tile a CTA of 256 threads, 64 k a step through shared memory, four-way byte dot
-// products into 32-bit integers.
+// This GPU's integer matrix rate is a small fraction of its fp16 rate, and tcgen05 has no
+// integer kind here.  Every int8 is a value of fp16, a product of two is below 2^14, and fp32
+// sums of whole numbers are exact below 2^24: so the operands become fp16 on the way to the tensor
+// core and the accumulator is the exact integer sum (rounded to fp32 where it passes 2^24).
+// Widening four bytes is five instructions: flip the sign bits, put 0x64 above each byte (1024 + u
+// in fp16), subtract 1024 + 128.
+//
+// Where the widened operands go decides the speed, because shared memory feeds everything
+// (128 bytes a cycle).  The weight is the MMA's A operand and goes to tensor memory, straight from the
+// registers that widened it; only the token rows (B) are written back to shared memory.  So a
+// tile is 128 or 256 weight rows (lanes) by TN <= 192 tokens (columns): accumulators 2 x 192
+// columns, two buffers of 2 x 32 columns for 64 k of A.  A 256 x 192 x 64 step is 768 cycles of
+// MMA against about 1000 of shared memory.
+//
+// Roles: 4 or 8 warps widen W (a weight row a thread), 4 warps x, one issues the TMA copies (128 k a
+// stage, 128-byte swizzle, zeros behind every edge), one the MMAs.  With few tiles K is
+// split over a cluster of up to 8 CTAs, whose fp32 partial tiles are summed in rank order through
+// distributed shared memory.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "kda_ops.h"
+#include "tc.cuh"
 
 namespace {
 
-constexpr int TILE = 64, KS = 64;
+constexpr int MAX_SPLIT = 8;   // portable cluster size
+constexpr int MAX_TN = 192;    // tokens of a tile
+constexpr int KSTAGE = 128;    // k a copy stage: the swizzle's 128 bytes
+constexpr int I8_MAX_STAGES = 6;
+constexpr int I8_MISC = 2048;
+constexpr int I8_SMEM = 227 * 1024;
+constexpr int X_WARPS = 4;
 
+// Device error bits, read and cleared by kda_linear_i8_check.
 __device__ unsigned g_i8_err;
 
 struct I8Args {
-  const int8_t *x, *w;
   const float *sx, *sw;
   __nv_bfloat16* y;
-  long long M, N, K, ldx, ldy;
+  long long M, N, K, ldy;
+  int tn;       // tokens of a tile, a multiple of 16
+  int tiles_m;  // token tiles
+  int stages;   // of the copy ring
+  int vec;      // y's rows take 8-byte stores
 };
 
-__global__ void __launch_bounds__(256) i8_tile_kernel(const I8Args a) {
-  __shared__ int xs[TILE][KS / 4 + 1], ws[TILE][KS / 4 + 1];
-  const long long n0 = (long long)blockIdx.x * TILE, m0 = (long long)blockIdx.y * TILE;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (long long k0 = 0; k0 < a.K; k0 += KS) {
-    const int r = threadIdx.x >> 2, c = threadIdx.x & 3;
-    const bool in = k0 + 16 * c < a.K;
-    int4 vx = make_int4(0, 0, 0, 0), vw = vx;
-    if (in && m0 + r < a.M) vx = *reinterpret_cast<const int4*>(a.x + (m0 + r) * a.ldx + k0 + 16 * c);
-    if (in && n0 + r < a.N) vw = *reinterpret_cast<const int4*>(a.w + (n0 + r) * a.K + k0 + 16 * c);
-    __syncthreads();
-    xs[r][4 * c] = vx.x, xs[r][4 * c + 1] = vx.y, xs[r][4 * c + 2] = vx.z, xs[r][4 * c + 3] = vx.w;
-    ws[r][4 * c] = vw.x, ws[r][4 * c + 1] = vw.y, ws[r][4 * c + 2] = vw.z, ws[r][4 * c + 3] = vw.w;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < KS / 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(xs[ty + 16 * i][k], ws[tx + 16 * j][k], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < a.M && n < a.N) a.y[m * a.ldy + n] = __float2bfloat16_rn((float)acc[i][j] * a.sx[m] * a.sw[n]);
-    }
+struct I8Misc {
+  float sx[MAX_TN];
+  uint32_t tmem;
+  int dead;
+  unsigned long long bars[2 * I8_MAX_STAGES + 6];
+};
+static_assert(sizeof(I8Misc) <= I8_MISC, "misc area");
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_id() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t local, unsigned rank) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote));
+  return v;
 }
 
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+// four int8 as two pairs of fp16
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+template <int MH>
+__global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
+    i8_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const I8Args a) {
+  constexpr int W_WARPS = 4 * MH, TM = 128 * MH, THREADS = 32 * (W_WARPS + X_WARPS + 2);
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
+  unsigned char* base_p = dyn + (base - smem_addr(dyn));
+  I8Misc& sm = *reinterpret_cast<I8Misc*>(base_p);
+  const uint32_t xbytes = (uint32_t)a.tn * 128u;         // 128 k of int8, and 64 k of fp16
+  const uint32_t xc = base + I8_MISC, ring = xc + 2 * xbytes;
+  const uint32_t stage_bytes = TM * 128 + xbytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned split = cluster_size(), rank = cluster_rank();
+  const long long grp = cluster_id();
+  // the token tiles of one weight tile are neighbours in launch order: all but the first find it in L2
+  const long long m0 = (grp % a.tiles_m) * a.tn, n0 = (grp / a.tiles_m) * TM;
+  const int total = (int)((a.K + KSTAGE - 1) / KSTAGE);
+  const int s_begin = (int)((long long)total * rank / split);
+  const int stages = (int)((long long)total * (rank + 1) / split) - s_begin;  // >= 1
+  const uint32_t bars = smem_addr(sm.bars);
+  auto full = [&](int i) { return bars + 8u * i; };
+  auto empty = [&](int i) { return bars + 8u * (I8_MAX_STAGES + i); };
+  auto conv_full = [&](int i) { return bars + 8u * (2 * I8_MAX_STAGES + i); };
+  auto conv_empty = [&](int i) { return bars + 8u * (2 * I8_MAX_STAGES + 2 + i); };
+  const uint32_t done = bars + 8u * (2 * I8_MAX_STAGES + 4);
+  if (threadIdx.x == 0) {
+    prefetch_map(&tx);
+    prefetch_map(&tw);
+    for (int i = 0; i < I8_MAX_STAGES; ++i) bar_init(full(i), 1), bar_init(empty(i), W_WARPS + X_WARPS);
+    for (int i = 0; i < 2; ++i) bar_init(conv_full(i), W_WARPS + X_WARPS), bar_init(conv_empty(i), 1);
+    bar_init(done, 1);
+    sm.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int i = threadIdx.x; i < a.tn; i += THREADS) sm.sx[i] = m0 + i < a.M ? a.sx[m0 + i] : 0.0f;
+  if (warp == W_WARPS + X_WARPS + 1) tmem_alloc(smem_addr(&sm.tmem), 512);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
+  volatile int* dead = &sm.dead;
+  auto t_acc = [&](int half) { return tmem + MAX_TN * half; };
+  auto t_a = [&](int buf, int half) { return tmem + 2 * MAX_TN + 64 * buf + 32 * half; };
+  bool ok = true;
+
+  if (warp < W_WARPS + X_WARPS) {
+    const bool is_w = warp < W_WARPS;
+    const int row = warp * 32 + lane;  // of the weight tile
+    for (int u = 0; u < 2 * stages; ++u) {  // 64 k each, two a stage
+      const int s = u >> 1, slot = s % a.stages, h = u & 1, buf = u & 1;
+      if (h == 0 && !(ok = warp_wait(full(slot), (s / a.stages) & 1, dead))) break;
+      if (u > 1 && !(ok = warp_wait(conv_empty(buf), ((u >> 1) & 1) ^ 1, dead))) break;
+      const uint32_t st = ring + slot * stage_bytes;
+      if (is_w) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 b = lds128(st + swz128(row, 4 * h + i));
+          widen(b.x, v[8 * i], v[8 * i + 1]);
+          widen(b.y, v[8 * i + 2], v[8 * i + 3]);
+          widen(b.z, v[8 * i + 4], v[8 * i + 5]);
+          widen(b.w, v[8 * i + 6], v[8 * i + 7]);
+        }
+        tc_after();
+        tmem_st(t_a(buf, warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16), v);
+        tmem_wait_st();
+        tc_before();
+      } else {
+        const uint32_t xs = st + TM * 128, xd = xc + buf * xbytes;
+        for (int e = threadIdx.x - 32 * W_WARPS; e < a.tn * 4; e += 32 * X_WARPS) {
+          const int r = (e >> 5) * 8 + (e & 7), i = (e >> 3) & 3;  // eight rows' chunks at a time: no bank conflicts
+          const uint4 b = lds128(xs + swz128(r, 4 * h + i));
+          uint4 c, d;
+          widen(b.x, c.x, c.y);
+          widen(b.y, c.z, c.w);
+          widen(b.z, d.x, d.y);
+          widen(b.w, d.z, d.w);
+          sts128(xd + swz128(r, 2 * i), c);
+          sts128(xd + swz128(r, 2 * i + 1), d);
+        }
+        fence_async();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(conv_full(buf));
+        if (h == 1) bar_arrive(empty(slot));
+      }
+    }
+  } else if (warp == W_WARPS + X_WARPS) {  // copies
+    for (int s = 0; s < stages; ++s) {
+      const int slot = s % a.stages;
+      if (s >= a.stages && !(ok = warp_wait(empty(slot), ((s / a.stages) & 1) ^ 1, dead))) break;
+      if (lane == 0) {
+        const uint32_t st = ring + slot * stage_bytes;
+        const int k = (s_begin + s) * KSTAGE;
+        bar_expect(full(slot), stage_bytes);
+        tma_load(st, &tw, k, (int)n0, full(slot));
+        tma_load(st + TM * 128, &tx, k, (int)m0, full(slot));
+      }
+      __syncwarp();
+    }
+  } else {  // matrix products
+    const uint32_t id = idesc_f16(128, a.tn);
+    for (int u = 0; u < 2 * stages; ++u) {
+      const int buf = u & 1;
+      if (!(ok = warp_wait(conv_full(buf), (u >> 1) & 1, dead))) break;
+      tc_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t b = desc_k(xc + buf * xbytes + 32 * k);
+#pragma unroll
+          for (int half = 0; half < MH; ++half) mma_ts(t_acc(half), t_a(buf, half) + 8 * k, b, id, u > 0 || k > 0);
+        }
+        mma_commit(conv_empty(buf));
+        if (u + 1 == 2 * stages) mma_commit(done);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) mma_commit(done);
+  }
+  if (!ok) {
+    *dead = 1;
+    if (lane == 0) atomicOr(&g_i8_err, KDA_ERR_TIMEOUT);
+  }
+  __syncwarp();
+  // everyone: the accumulators are final
+  if (!warp_wait(done, 0, dead) && lane == 0) atomicOr(&g_i8_err, KDA_ERR_TIMEOUT);
+  tc_after();
+  __syncthreads();
+  if (*dead) {
+    // copies that were issued and not waited for land before the memory goes (~10 ms)
+    const long long c0 = clock64();
+    while (clock64() - c0 < 20000000ll) {
+    }
+  }
+  __syncthreads();
+
+  // Read-out, by W's warps: thread = weight row (an output column), accumulator columns = tokens.  The tile goes
+  // through shared memory (the drained ring) so that the stores are along y's rows.
+  const int rows = a.M - m0 < a.tn ? (int)(a.M - m0) : a.tn;      // tokens of this tile
+  const int cols = a.N - n0 < TM ? (int)(a.N - n0) : TM;
+  if (split == 1) {
+    constexpr int LD = TM + 8;  // bf16 a row
+    __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(base_p + I8_MISC);
+    if (warp < W_WARPS) {
+      const int n = threadIdx.x;
+      const float sw = n < cols ? a.sw[n0 + n] : 0.0f;
+      for (int c = 0; c < rows; c += 16) {
+        uint32_t v[16];
+        tmem_ld(t_acc(warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          tile[(c + i) * LD + n] = __float2bfloat16_rn(__uint_as_float(v[i]) * sm.sx[c + i] * sw);
+      }
+      tc_before();
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += THREADS / 32) {
+      __nv_bfloat16* y = a.y + (m0 + r) * a.ldy + n0;
+      for (int c = 4 * lane; c < cols; c += 128) {
+        const uint2 v = *reinterpret_cast<const uint2*>(tile + r * LD + c);
+        if (a.vec && c + 4 <= cols) {
+          *reinterpret_cast<uint2*>(y + c) = v;
+        } else {
+          const __nv_bfloat16* e = tile + r * LD + c;
+          for (int i = 0; i < 4 && c + i < cols; ++i) y[c + i] = e[i];
+        }
+      }
+    }
+  } else {
+    constexpr int LD = 132;  // fp32 a row of one half's 128 weight rows
+    float* red = reinterpret_cast<float*>(base_p + I8_MISC);
+    for (int half = 0; half < MH; ++half) {
+      if (warp < W_WARPS && (warp >> 2) == half) {
+        const int n = (warp & 3) * 32 + lane;
+        for (int c = 0; c < rows; c += 16) {
+          uint32_t v[16];
+          tmem_ld(t_acc(half) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) red[(c + i) * LD + n] = __uint_as_float(v[i]);
+        }
+        tc_before();
+      }
+      cluster_sync();
+      // this CTA's share: groups of four columns, row by row
+      const int e_end = (int)((long long)rows * 32 * (rank + 1) / split);
+      for (int e = (int)((long long)rows * 32 * rank / split) + threadIdx.x; e < e_end; e += THREADS) {
+        const int r = e >> 5, c = (e & 31) * 4, n = half * 128 + c;
+        if (n >= cols) continue;
+        const uint32_t at = smem_addr(red + r * LD + c);
+        float4 t[MAX_SPLIT];
+#pragma unroll
+        for (int q = 0; q < MAX_SPLIT; ++q)
+          t[q] = (unsigned)q < split ? peer_f32x4(at, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 v = t[0];
+#pragma unroll
+        for (int q = 1; q < MAX_SPLIT; ++q) v.x += t[q].x, v.y += t[q].y, v.z += t[q].z, v.w += t[q].w;
+        const float sx = sm.sx[r];
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        __nv_bfloat16* y = a.y + (m0 + r) * a.ldy + n0 + n;
+        if (a.vec && n + 4 <= cols) {
+          const float* sw = a.sw + n0 + n;
+          *reinterpret_cast<uint2*>(y) =
+              make_uint2(pack_bf(f[0] * sx * sw[0], f[1] * sx * sw[1]), pack_bf(f[2] * sx * sw[2], f[3] * sx * sw[3]));
+        } else {
+          for (int i = 0; i < 4 && n + i < cols; ++i) y[i] = __float2bfloat16_rn(f[i] * sx * a.sw[n0 + n + i]);
+        }
+      }
+      cluster_sync();  // the peers have read this CTA's partials
+    }
+  }
+  __syncthreads();
+  if (warp == W_WARPS + X_WARPS + 1) {
+    tc_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// A launch: weight-row halves, tokens a tile, K split.
+struct I8Plan {
+  int mh = 1, tn = 16, split = 1;
+  double cost = 1e300;
+};
+
+int ring_stages(int mh, int tn) {
+  const int room = I8_SMEM - 1024 - I8_MISC - 2 * tn * 128;
+  const int n = room / ((128 * mh + tn) * 128);
+  return n < I8_MAX_STAGES ? n : I8_MAX_STAGES;
+}
+
+template <int MH>
+void i8_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long long ctas, int split, cudaStream_t st) {
+  *cfg = {};
+  cfg->gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg->blockDim = dim3(32 * (4 * MH + X_WARPS + 2), 1, 1);
+  cfg->dynamicSmemBytes = I8_SMEM;
+  cfg->stream = st;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)split;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// Clusters of c CTAs that the device holds at once (a cluster stays within one GPC, so fewer
+// than SMs / c), looked up once per device; 0 if that fails.
+template <int MH>
+int clusters_held(int dev, int c) {
+  static std::atomic<int> cache[64][MAX_SPLIT + 1];
+  int held = dev < 64 ? cache[dev][c].load(std::memory_order_relaxed) : 0;
+  if (held <= 0) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    i8_config<MH>(&cfg, attr, c, c, nullptr);
+    // the shared-memory attribute is per device
+    if (cudaFuncSetAttribute(i8_kernel<MH>, cudaFuncAttributeMaxDynamicSharedMemorySize, I8_SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&held, i8_kernel<MH>, &cfg) != cudaSuccess)
+      return 0;
+    const int cap = sm_count(dev) / c;
+    if (held > cap) held = cap;
+    if (held > 0 && dev < 64) cache[dev][c].store(held, std::memory_order_relaxed);
+  }
+  return held;
+}
+
+// The launch that the model rates fastest: waves of clusters x (a CTA's 64-k steps + its fixed part).
+I8Plan i8_plan(long long M, long long N, long long K, int dev) {
+  I8Plan best;
+  const long long steps = (K + 63) / 64, stages = (K + KSTAGE - 1) / KSTAGE;
+  for (int mh = 1; mh <= 2; ++mh) {
+    const long long tiles_n = (N + 128 * mh - 1) / (128 * mh);
+    for (int parts = 0; parts < 8; ++parts) {
+      // tokens in the fewest tiles and up to 7 more, all of about one size
+      const long long want = (M + MAX_TN - 1) / MAX_TN + parts;
+      const int tn = (int)(((M + want - 1) / want + 15) / 16 * 16);
+      const long long groups = tiles_n * ((M + tn - 1) / tn);
+      for (int c = 1; c <= MAX_SPLIT && c <= stages; ++c) {
+        const int held = mh == 2 ? clusters_held<2>(dev, c) : clusters_held<1>(dev, c);
+        if (held <= 0) continue;
+        const double waves = (double)((groups + held - 1) / held);
+        const double mma = 0.021 * tn * mh / 8.0, feed = 0.10 * mh + 0.0006 * tn;
+        const double step = mma > feed ? mma : feed;
+        const double cost =
+            waves * ((double)steps / c * step + 5.0 + 0.01 * tn * mh + (c > 1 ? 1.5 + 0.01 * tn * mh : 0.0));
+        if (cost < best.cost * (1.0 - 1e-9)) best.cost = cost, best.mh = mh, best.tn = tn, best.split = c;
+      }
+      if (tn <= 16) break;
+    }
+  }
+  return best;
+}
+
+template <int MH>
+int i8_launch(const void* x, long long ldx, const void* w, I8Args a, const I8Plan& p, cudaStream_t st) {
+  CUtensorMap tx, tw;
+  const CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapSwizzle s = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!encode_2d(&tx, t, x, a.M, a.K, ldx, KSTAGE, p.tn, s) ||
+      !encode_2d(&tw, t, w, a.N, a.K, a.K, KSTAGE, 128 * MH, s))
+    return KDA_ECUDA;
+  a.tn = p.tn;
+  a.tiles_m = (int)((a.M + p.tn - 1) / p.tn);
+  a.stages = ring_stages(MH, p.tn);
+  const long long groups = (a.N + 128 * MH - 1) / (128 * MH) * a.tiles_m;
+  if (groups * p.split > 0x7fffffffLL) return KDA_EINVAL;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[1];
+  i8_config<MH>(&cfg, attr, groups * p.split, p.split, st);
+  if (cudaLaunchKernelEx(&cfg, i8_kernel<MH>, tx, tw, a) != cudaSuccess) return KDA_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
+}
 
 }  // namespace
 
@@ -64,18 +422,23 @@ extern "C" int kda_linear_i8(const void* x, long long rows, long long ldx, const
   if (rows < 0 || N < 1 || K < 16 || K % 16 != 0) return KDA_EINVAL;
   if (rows == 0) return KDA_OK;
   if (!x || !x_scales || !w || !w_scales || !y || ldx < K || ldx % 16 != 0 || ldy < N) return KDA_EINVAL;
-  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+  if (!ptr_aligned(x, 16) || !ptr_aligned(w, 16) || !ptr_aligned(y, 2) || !ptr_aligned(x_scales, 4) ||
+      !ptr_aligned(w_scales, 4))
     return KDA_EINVAL;
-  if (K > 131072 || N > 0x7fffffffLL || rows > 65535LL * TILE) return KDA_EINVAL;
-  I8Args a;
-  a.x = static_cast<const int8_t*>(x);
-  a.w = static_cast<const int8_t*>(w);
+  // tensor-map coordinates fit 32 bits
+  if (K > 0x7fffff00LL || N > 0x7fffff00LL || rows > 0x7fffff00LL) return KDA_EINVAL;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ECUDA;
+  if (!on_device(x, dev) || !on_device(w, dev) || !on_device(y, dev)) return KDA_EINVAL;
+  I8Args a = {};
   a.sx = x_scales, a.sw = w_scales;
   a.y = static_cast<__nv_bfloat16*>(y);
-  a.M = rows, a.N = N, a.K = K, a.ldx = ldx, a.ldy = ldy;
-  const dim3 grid((unsigned)((N + TILE - 1) / TILE), (unsigned)((rows + TILE - 1) / TILE));
-  i8_tile_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(cuda_stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
+  a.M = rows, a.N = N, a.K = K, a.ldy = ldy;
+  a.vec = ptr_aligned(y, 8) && ldy % 4 == 0;
+  const I8Plan p = i8_plan(rows, N, K, dev);
+  if (p.cost >= 1e300) return KDA_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  return p.mh == 2 ? i8_launch<2>(x, ldx, w, a, p, st) : i8_launch<1>(x, ldx, w, a, p, st);
 }
 
 extern "C" int kda_linear_i8_check(void* cuda_stream, unsigned* device_flags) {

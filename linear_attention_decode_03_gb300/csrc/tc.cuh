@@ -109,8 +109,11 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t a, uint32_t box) {
   return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)(box >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
-// Instruction descriptor, kind::f16: fp32 accumulator (bits 4-5 = 1), bf16 A and B (bits
-// 7-9, 10-12 = 1), MN-major A / B at bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+// Instruction descriptors, kind::f16: fp32 accumulator (bits 4-5 = 1), A and B both bf16 (bits
+// 7-9, 10-12 = 1) or both fp16 (0), MN-major A / B at bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
@@ -189,6 +192,16 @@ __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&v)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
 // 16 columns of 16 lanes (the warp's quarter, + 0 or + 16 in the address): register 2 g + i of
 // thread t goes to lane 8 i + t / 4, column 4 g + t % 4
 __device__ __forceinline__ void tmem_st_frag(uint32_t a, const uint32_t (&v)[8]) {
