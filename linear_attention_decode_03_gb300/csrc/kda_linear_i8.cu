@@ -16,7 +16,7 @@
 // columns, two buffers of 2 x 32 columns for 64 k of A.  A 256 x 192 x 64 step is 768 cycles of
 // MMA against about 1000 of shared memory.
 //
-// Roles: 4 or 8 warps widen W (a weight row a thread), 4 warps x, one issues the TMA copies (128 k a
+// Roles: 4 or 8 warps widen W (a weight row a thread), 8 warps x, one issues the TMA copies (128 k a
 // stage, 128-byte swizzle, zeros behind every edge), one the MMAs.  With few tiles K is
 // split over a cluster of up to 8 CTAs, whose fp32 partial tiles are summed in rank order through
 // distributed shared memory.
@@ -36,7 +36,8 @@ constexpr int KSTAGE = 128;    // k a copy stage: the swizzle's 128 bytes
 constexpr int I8_MAX_STAGES = 6;
 constexpr int I8_MISC = 2048;
 constexpr int I8_SMEM = 227 * 1024;
-constexpr int X_WARPS = 4;
+constexpr int X_WARPS = 8;
+constexpr int X_CHUNKS = MAX_TN * 4 / (32 * X_WARPS);  // 16-byte chunks of 64 k of x that a thread widens
 
 // Device error bits, read and cleared by kda_linear_i8_check.
 __device__ unsigned g_i8_err;
@@ -144,12 +145,14 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
   bool ok = true;
 
   if (warp < W_WARPS + X_WARPS) {
+    // Each unit of 64 k is read and (W) widened before the wait for its buffer: the chain from one
+    // unit's buffer to the next is only the store.
     const bool is_w = warp < W_WARPS;
-    const int row = warp * 32 + lane;  // of the weight tile
-    for (int u = 0; u < 2 * stages; ++u) {  // 64 k each, two a stage
+    const int row = warp * 32 + lane;            // of the weight tile
+    const int e0 = threadIdx.x - 32 * W_WARPS;   // of the x tile's 16-byte chunks, 32 X_WARPS apart
+    for (int u = 0; u < 2 * stages; ++u) {       // two a stage
       const int s = u >> 1, slot = s % a.stages, h = u & 1, buf = u & 1;
       if (h == 0 && !(ok = warp_wait(full(slot), (s / a.stages) & 1, dead))) break;
-      if (u > 1 && !(ok = warp_wait(conv_empty(buf), ((u >> 1) & 1) ^ 1, dead))) break;
       const uint32_t st = ring + slot * stage_bytes;
       if (is_w) {
         uint32_t v[32];
@@ -161,22 +164,34 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
           widen(b.z, v[8 * i + 4], v[8 * i + 5]);
           widen(b.w, v[8 * i + 6], v[8 * i + 7]);
         }
+        if (u > 1 && !(ok = warp_wait(conv_empty(buf), ((u >> 1) & 1) ^ 1, dead))) break;
         tc_after();
         tmem_st(t_a(buf, warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16), v);
         tmem_wait_st();
         tc_before();
       } else {
         const uint32_t xs = st + TM * 128, xd = xc + buf * xbytes;
-        for (int e = threadIdx.x - 32 * W_WARPS; e < a.tn * 4; e += 32 * X_WARPS) {
-          const int r = (e >> 5) * 8 + (e & 7), i = (e >> 3) & 3;  // eight rows' chunks at a time: no bank conflicts
-          const uint4 b = lds128(xs + swz128(r, 4 * h + i));
-          uint4 c, d;
-          widen(b.x, c.x, c.y);
-          widen(b.y, c.z, c.w);
-          widen(b.z, d.x, d.y);
-          widen(b.w, d.z, d.w);
-          sts128(xd + swz128(r, 2 * i), c);
-          sts128(xd + swz128(r, 2 * i + 1), d);
+        uint4 b[X_CHUNKS];
+#pragma unroll
+        for (int j = 0; j < X_CHUNKS; ++j) {
+          const int e = e0 + 32 * X_WARPS * j;
+          // eight rows' chunks at a time: no bank conflicts
+          if (e < a.tn * 4) b[j] = lds128(xs + swz128((e >> 5) * 8 + (e & 7), 4 * h + ((e >> 3) & 3)));
+        }
+        if (u > 1 && !(ok = warp_wait(conv_empty(buf), ((u >> 1) & 1) ^ 1, dead))) break;
+#pragma unroll
+        for (int j = 0; j < X_CHUNKS; ++j) {
+          const int e = e0 + 32 * X_WARPS * j;
+          if (e < a.tn * 4) {
+            const int r = (e >> 5) * 8 + (e & 7), i = (e >> 3) & 3;
+            uint4 c, d;
+            widen(b[j].x, c.x, c.y);
+            widen(b[j].y, c.z, c.w);
+            widen(b[j].z, d.x, d.y);
+            widen(b[j].w, d.z, d.w);
+            sts128(xd + swz128(r, 2 * i), c);
+            sts128(xd + swz128(r, 2 * i + 1), d);
+          }
         }
         fence_async();
       }
