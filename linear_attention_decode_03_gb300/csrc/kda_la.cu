@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       for (int j = 0; j < 4; ++j) g[j] = 4 * lane + j < n ? a.g[(t0 + j) * a.ldg + h] : 0.0f;
       auto load = [&](int full, int empty, uint32_t dst, const CUtensorMap* map, int col) {
         if (c > 1 && !(ok = wait(empty + (c & 1), ((c >> 1) & 1) ^ 1))) return;  // its reader two chunks ago
-        if (lane == 0) {
+        if (elect()) {
           const uint32_t b = bar(full + (c & 1));
           bar_expect(b, TILE);
           tma_load(dst, map, col, row, b);
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       if (!LOCAL) {
         if (!(ok = wait(FULL_Q + ph, ph2) && wait(FULL_K + ph, ph2))) break;
         tc_after();
-        if (lane == 0) {
+        if (elect()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint32_t at = (k >> 2) * BOX + 32 * (k & 3);
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       // (S_IN: the threads have read the chunk before's K'^T V, too)
       if (!(ok = wait(S_IN, ph) && (LOCAL || c == 0 || wait(O_READ, ph ^ 1)))) break;
       tc_after();
-      if (!LOCAL && lane == 0) {
+      if (!LOCAL && elect()) {
         if (from_state) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       __syncwarp();
       if (!(ok = wait(KP, ph) && wait(FULL_V + ph, ph2))) break;
       tc_after();
-      if (lane == 0 && want) {
+      if (want && elect()) {
         if (LOCAL) delta(t_lo(c), true);  // smallest first
         delta(t_mid(c), !LOCAL);
         delta(t_hi(c), false);
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       if (!LOCAL) {
         if (!(ok = wait(P_IN, ph))) break;
         tc_after();
-        if (lane == 0) {
+        if (elect()) {
           if (want) {
             if (!BF) delta(t_lo(c), false);
             mma_commit(bar(DELTA));
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (*dead && threadIdx.x == 32 * (COMPUTE_WARPS + 1)) {
+  if (*dead && warp == COMPUTE_WARPS + 1 && elect()) {
     // what is still in flight lands before the memory goes: the MMAs, then the copies nobody has
     // waited for (they take microseconds; ~10 ms)
     int never = 0;

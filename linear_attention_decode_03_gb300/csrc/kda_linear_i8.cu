@@ -16,8 +16,10 @@
 // columns, two buffers of 2 x 32 columns for 64 k of A.  A 256 x 192 x 64 step is 768 cycles of
 // MMA against about 1000 of shared memory.
 //
-// Roles: 4 or 8 warps widen W (a weight row a thread), 8 warps x, one issues the TMA copies (128 k a
-// stage, 128-byte swizzle, zeros behind every edge), one the MMAs.  With few tiles K is
+// Roles: two groups of warps widen the even and the odd units of 64 k (one alone took 1000
+// cycles a unit, wait, read, widen and store one after the other), 4 or 8 of them W (a weight row a
+// thread), 4 x; one warp issues the TMA copies (128 k a stage, 128-byte swizzle, zeros behind
+// every edge), one the MMAs.  With few tiles K is
 // split over a cluster of up to 8 CTAs, whose fp32 partial tiles are summed in rank order through
 // distributed shared memory.
 #include <cuda_bf16.h>
@@ -36,7 +38,7 @@ constexpr int KSTAGE = 128;    // k a copy stage: the swizzle's 128 bytes
 constexpr int I8_MAX_STAGES = 6;
 constexpr int I8_MISC = 2048;
 constexpr int I8_SMEM = 227 * 1024;
-constexpr int X_WARPS = 8;
+constexpr int X_WARPS = 4;     // of each of the two groups
 constexpr int X_CHUNKS = MAX_TN * 4 / (32 * X_WARPS);  // 16-byte chunks of 64 k of x that a thread widens
 
 // Device error bits, read and cleared by kda_linear_i8_check.
@@ -100,9 +102,9 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 
 template <int MH>
-__global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
+__global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
     i8_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw, const I8Args a) {
-  constexpr int W_WARPS = 4 * MH, TM = 128 * MH, THREADS = 32 * (W_WARPS + X_WARPS + 2);
+  constexpr int W_WARPS = 4 * MH, GROUP = W_WARPS + X_WARPS, TM = 128 * MH, THREADS = 32 * (2 * GROUP + 2);
   extern __shared__ __align__(1024) unsigned char dyn[];
   const uint32_t base = (smem_addr(dyn) + 1023u) & ~1023u;
   unsigned char* base_p = dyn + (base - smem_addr(dyn));
@@ -127,14 +129,14 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
   if (threadIdx.x == 0) {
     prefetch_map(&tx);
     prefetch_map(&tw);
-    for (int i = 0; i < I8_MAX_STAGES; ++i) bar_init(full(i), 1), bar_init(empty(i), W_WARPS + X_WARPS);
-    for (int i = 0; i < 2; ++i) bar_init(conv_full(i), W_WARPS + X_WARPS), bar_init(conv_empty(i), 1);
+    for (int i = 0; i < I8_MAX_STAGES; ++i) bar_init(full(i), 1), bar_init(empty(i), 2 * GROUP);
+    for (int i = 0; i < 2; ++i) bar_init(conv_full(i), GROUP), bar_init(conv_empty(i), 1);
     bar_init(done, 1);
     sm.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = threadIdx.x; i < a.tn; i += THREADS) sm.sx[i] = m0 + i < a.M ? a.sx[m0 + i] : 0.0f;
-  if (warp == W_WARPS + X_WARPS + 1) tmem_alloc(smem_addr(&sm.tmem), 512);
+  if (warp == 2 * GROUP + 1) tmem_alloc(smem_addr(&sm.tmem), 512);
   tc_before();
   __syncthreads();
   tc_after();
@@ -144,29 +146,29 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
   auto t_a = [&](int buf, int half) { return tmem + 2 * MAX_TN + 64 * buf + 32 * half; };
   bool ok = true;
 
-  if (warp < W_WARPS + X_WARPS) {
-    // Each unit of 64 k is read and (W) widened before the wait for its buffer: the chain from one
-    // unit's buffer to the next is only the store.
-    const bool is_w = warp < W_WARPS;
-    const int row = warp * 32 + lane;            // of the weight tile
-    const int e0 = threadIdx.x - 32 * W_WARPS;   // of the x tile's 16-byte chunks, 32 X_WARPS apart
-    for (int u = 0; u < 2 * stages; ++u) {       // two a stage
-      const int s = u >> 1, slot = s % a.stages, h = u & 1, buf = u & 1;
-      if (h == 0 && !(ok = warp_wait(full(slot), (s / a.stages) & 1, dead))) break;
+  const int buf = warp >= GROUP ? 1 : 0;         // the group, its half of each stage's k, its buffers
+  const int gw = warp - buf * GROUP;             // the warp in its group
+  if (warp < 2 * GROUP) {
+    // Each unit is read and (W) widened before the wait for its buffer.
+    const int row = gw * 32 + lane;              // of the weight tile
+    const int e0 = (gw - W_WARPS) * 32 + lane;   // of the x tile's 16-byte chunks, 32 X_WARPS apart
+    for (int s = 0; s < stages; ++s) {
+      const int slot = s % a.stages;
+      if (!(ok = warp_wait(full(slot), (s / a.stages) & 1, dead))) break;
       const uint32_t st = ring + slot * stage_bytes;
-      if (is_w) {
+      if (gw < W_WARPS) {
         uint32_t v[32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 b = lds128(st + swz128(row, 4 * h + i));
+          const uint4 b = lds128(st + swz128(row, 4 * buf + i));
           widen(b.x, v[8 * i], v[8 * i + 1]);
           widen(b.y, v[8 * i + 2], v[8 * i + 3]);
           widen(b.z, v[8 * i + 4], v[8 * i + 5]);
           widen(b.w, v[8 * i + 6], v[8 * i + 7]);
         }
-        if (u > 1 && !(ok = warp_wait(conv_empty(buf), ((u >> 1) & 1) ^ 1, dead))) break;
+        if (s > 0 && !(ok = warp_wait(conv_empty(buf), (s & 1) ^ 1, dead))) break;
         tc_after();
-        tmem_st(t_a(buf, warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16), v);
+        tmem_st(t_a(buf, gw >> 2) + ((uint32_t)((gw & 3) * 32) << 16), v);
         tmem_wait_st();
         tc_before();
       } else {
@@ -176,9 +178,9 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
         for (int j = 0; j < X_CHUNKS; ++j) {
           const int e = e0 + 32 * X_WARPS * j;
           // eight rows' chunks at a time: no bank conflicts
-          if (e < a.tn * 4) b[j] = lds128(xs + swz128((e >> 5) * 8 + (e & 7), 4 * h + ((e >> 3) & 3)));
+          if (e < a.tn * 4) b[j] = lds128(xs + swz128((e >> 5) * 8 + (e & 7), 4 * buf + ((e >> 3) & 3)));
         }
-        if (u > 1 && !(ok = warp_wait(conv_empty(buf), ((u >> 1) & 1) ^ 1, dead))) break;
+        if (s > 0 && !(ok = warp_wait(conv_empty(buf), (s & 1) ^ 1, dead))) break;
 #pragma unroll
         for (int j = 0; j < X_CHUNKS; ++j) {
           const int e = e0 + 32 * X_WARPS * j;
@@ -198,14 +200,14 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
       __syncwarp();
       if (lane == 0) {
         bar_arrive(conv_full(buf));
-        if (h == 1) bar_arrive(empty(slot));
+        bar_arrive(empty(slot));
       }
     }
-  } else if (warp == W_WARPS + X_WARPS) {  // copies
+  } else if (warp == 2 * GROUP) {  // copies
     for (int s = 0; s < stages; ++s) {
       const int slot = s % a.stages;
       if (s >= a.stages && !(ok = warp_wait(empty(slot), ((s / a.stages) & 1) ^ 1, dead))) break;
-      if (lane == 0) {
+      if (elect()) {
         const uint32_t st = ring + slot * stage_bytes;
         const int k = (s_begin + s) * KSTAGE;
         bar_expect(full(slot), stage_bytes);
@@ -216,11 +218,11 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
     }
   } else {  // matrix products
     const uint32_t id = idesc_f16(128, a.tn);
-    for (int u = 0; u < 2 * stages; ++u) {
+    for (int u = 0; u < 2 * stages; ++u) {  // 64 k each
       const int buf = u & 1;
       if (!(ok = warp_wait(conv_full(buf), (u >> 1) & 1, dead))) break;
       tc_after();
-      if (lane == 0) {
+      if (elect()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint64_t b = desc_k(xc + buf * xbytes + 32 * k);
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
       }
       __syncwarp();
     }
-    if (!ok && lane == 0) mma_commit(done);
+    if (!ok && elect()) mma_commit(done);
   }
   if (!ok) {
     *dead = 1;
@@ -251,19 +253,19 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
   }
   __syncthreads();
 
-  // Read-out, by W's warps: thread = weight row (an output column), accumulator columns = tokens.  The tile goes
+  // Read-out, by W's warps of both groups (16 columns in turn): thread = weight row (an output column), accumulator columns = tokens.  The tile goes
   // through shared memory (the drained ring) so that the stores are along y's rows.
   const int rows = a.M - m0 < a.tn ? (int)(a.M - m0) : a.tn;      // tokens of this tile
   const int cols = a.N - n0 < TM ? (int)(a.N - n0) : TM;
   if (split == 1) {
     constexpr int LD = TM + 8;  // bf16 a row
     __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(base_p + I8_MISC);
-    if (warp < W_WARPS) {
-      const int n = threadIdx.x;
+    if (warp < 2 * GROUP && gw < W_WARPS) {
+      const int n = gw * 32 + lane;
       const float sw = n < cols ? a.sw[n0 + n] : 0.0f;
-      for (int c = 0; c < rows; c += 16) {
+      for (int c = 16 * buf; c < rows; c += 32) {
         uint32_t v[16];
-        tmem_ld(t_acc(warp >> 2) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
+        tmem_ld(t_acc(gw >> 2) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
         tmem_wait_ld(v);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -288,9 +290,9 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
     constexpr int LD = 132;  // fp32 a row of one half's 128 weight rows
     float* red = reinterpret_cast<float*>(base_p + I8_MISC);
     for (int half = 0; half < MH; ++half) {
-      if (warp < W_WARPS && (warp >> 2) == half) {
-        const int n = (warp & 3) * 32 + lane;
-        for (int c = 0; c < rows; c += 16) {
+      if (warp < 2 * GROUP && gw < W_WARPS && (gw >> 2) == half) {
+        const int n = (gw & 3) * 32 + lane;
+        for (int c = 16 * buf; c < rows; c += 32) {
           uint32_t v[16];
           tmem_ld(t_acc(half) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
           tmem_wait_ld(v);
@@ -328,10 +330,111 @@ __global__ void __launch_bounds__(32 * (4 * MH + X_WARPS + 2), 1)
     }
   }
   __syncthreads();
-  if (warp == W_WARPS + X_WARPS + 1) {
+  if (warp == 2 * GROUP + 1) {
     tc_after();
     tmem_free(tmem, 512);
   }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: mma.sync (m16n8k16, fp16) with 16 weight rows as M and 8 NT tokens as N, operands straight
+// from global memory into fragments.  The product sums over k in any order, so a thread's 16
+// contiguous bytes of a row serve as its four k of four steps (lane l: rows l / 4 and + 8, bytes
+// 16 (l % 4) of 64), for W and x alike: no shared memory, no shuffles.  The 8 warps of a CTA take the
+// 64-k chunks in turn and add their partial tiles through shared memory, in warp order.  The
+// bound is the weight's bytes; UNROLL chunks of it are in flight a warp, and the CTAS resident
+// CTAs cover each other's latency (loading ahead of the products measured slower, 12.2 against
+// 10.5 us for 1 x 7168 x 6284: the registers cost more CTAs than that hides).
+constexpr int ROWS_WARPS = 8;
+
+// 16 bytes, zeros where `in` is false; KEEP: in L1 (x, which every CTA of the SM reads).
+template <bool KEEP>
+__device__ __forceinline__ uint4 load16(const int8_t* p, bool in) {
+  uint4 v;
+  if (KEEP)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)in));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)in));
+  return v;
+}
+
+template <int NT, int UNROLL, int CTAS>
+__global__ void __launch_bounds__(32 * ROWS_WARPS, CTAS)
+    i8_rows_kernel(const int8_t* __restrict__ x, long long ldx, const int8_t* __restrict__ w, const I8Args a) {
+  __shared__ float red[ROWS_WARPS][128 * NT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const long long n0 = (long long)blockIdx.x * 16;
+  const int chunks = (int)((a.K + 63) / 64);
+  const bool in0 = n0 + g < a.N, in1 = n0 + g + 8 < a.N;
+  const int8_t* w0 = w + (n0 + g) * a.K + 16 * t;
+  const int8_t* w1 = w0 + 8 * a.K;
+  const int8_t* xp = x + g * ldx + 16 * t;
+  float acc[NT][4] = {};
+  for (int c0 = warp; c0 < chunks; c0 += ROWS_WARPS * UNROLL) {
+    uint4 wa[UNROLL], wb[UNROLL], xb[UNROLL][NT];
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      const long long k = 64ll * (c0 + ROWS_WARPS * j);
+      const bool in = k + 16 * t < a.K;
+      wa[j] = load16<false>(w0 + k, in && in0);
+      wb[j] = load16<false>(w1 + k, in && in1);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) xb[j][i] = load16<true>(xp + 8 * i * ldx + k, in && g + 8 * i < a.M);
+    }
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      const uint32_t pa[4] = {wa[j].x, wa[j].y, wa[j].z, wa[j].w}, pb[4] = {wb[j].x, wb[j].y, wb[j].z, wb[j].w};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        uint32_t a0, a1, a2, a3;
+        widen(pa[s], a0, a2);
+        widen(pb[s], a1, a3);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const uint32_t px[4] = {xb[j][i].x, xb[j][i].y, xb[j][i].z, xb[j][i].w};
+          uint32_t b0, b1;
+          widen(px[s], b0, b1);
+          asm volatile(
+              "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+              "{%0, %1, %2, %3};"
+              : "+f"(acc[i][0]), "+f"(acc[i][1]), "+f"(acc[i][2]), "+f"(acc[i][3])
+              : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        }
+      }
+    }
+  }
+  // accumulator: 0, 1 at weight row g, tokens 2 t, + 1; 2, 3 eight weight rows down
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[warp][(8 * i + 2 * t + (j & 1)) * 16 + g + 8 * (j >> 1)] = acc[i][j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 128 * NT; e += 32 * ROWS_WARPS) {
+    const int m = e >> 4;
+    const long long n = n0 + (e & 15);
+    if (m >= a.M || n >= a.N) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < ROWS_WARPS; ++q) v += red[q][e];
+    a.y[m * a.ldy + n] = __float2bfloat16_rn(v * a.sx[m] * a.sw[n]);
+  }
+}
+
+template <int NT, int UNROLL, int CTAS>
+int i8_rows_launch(const void* x, long long ldx, const void* w, const I8Args& a, cudaStream_t st) {
+  i8_rows_kernel<NT, UNROLL, CTAS><<<(unsigned)((a.N + 15) / 16), 32 * ROWS_WARPS, 0, st>>>(
+      static_cast<const int8_t*>(x), ldx, static_cast<const int8_t*>(w), a);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
 }
 
 // A launch: weight-row halves, tokens a tile, K split.
@@ -350,7 +453,7 @@ template <int MH>
 void i8_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long long ctas, int split, cudaStream_t st) {
   *cfg = {};
   cfg->gridDim = dim3((unsigned)ctas, 1, 1);
-  cfg->blockDim = dim3(32 * (4 * MH + X_WARPS + 2), 1, 1);
+  cfg->blockDim = dim3(32 * (2 * (4 * MH + X_WARPS) + 2), 1, 1);
   cfg->dynamicSmemBytes = I8_SMEM;
   cfg->stream = st;
   attr->id = cudaLaunchAttributeClusterDimension;
@@ -450,9 +553,11 @@ extern "C" int kda_linear_i8(const void* x, long long rows, long long ldx, const
   a.y = static_cast<__nv_bfloat16*>(y);
   a.M = rows, a.N = N, a.K = K, a.ldy = ldy;
   a.vec = ptr_aligned(y, 8) && ldy % 4 == 0;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (rows <= 8) return i8_rows_launch<1, 3, 4>(x, ldx, w, a, st);
+  if (rows <= 16) return i8_rows_launch<2, 2, 3>(x, ldx, w, a, st);
   const I8Plan p = i8_plan(rows, N, K, dev);
   if (p.cost >= 1e300) return KDA_ECUDA;
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   return p.mh == 2 ? i8_launch<2>(x, ldx, w, a, p, st) : i8_launch<1>(x, ldx, w, a, p, st);
 }
 
