@@ -12,9 +12,10 @@
 // Where the widened operands go decides the speed, because shared memory feeds everything
 // (128 bytes a cycle).  The weight is the MMA's A operand and goes to tensor memory, straight from the
 // registers that widened it; only the token rows (B) are written back to shared memory.  So a
-// tile is 128 or 256 weight rows (lanes) by TN <= 192 tokens (columns): accumulators 2 x 192
-// columns, two buffers of 2 x 32 columns for 64 k of A.  A 256 x 192 x 64 step is 768 cycles of
-// MMA against about 1000 of shared memory.
+// tile is 128 or 256 weight rows (lanes) by TN <= 192 tokens (columns); a 256 x 160 x 64 step is 640
+// cycles of MMA against about 850 of shared memory.  Widened units (64 k) have three buffers where tensor
+// memory has the room (TN <= 160), else two: with two the way from one unit's last MMA to the first on
+// the same buffer (store, fence, barriers: 850 cycles) shows, 0.64 against 0.52 us a step.
 //
 // Roles: two groups of warps widen the even and the odd units of 64 k (one alone took 1000
 // cycles a unit, wait, read, widen and store one after the other), 4 or 8 of them W (a weight row a
@@ -34,6 +35,8 @@ namespace {
 
 constexpr int MAX_SPLIT = 8;   // portable cluster size
 constexpr int MAX_TN = 192;    // tokens of a tile
+constexpr int MAX_BUFS = 3;    // of widened units
+constexpr int MAX_TN3 = 160;   // tokens of a tile with 3 of them: 2 x 160 + 3 x 64 columns of tensor memory (2 x 192 + 2 x 64)
 constexpr int KSTAGE = 128;    // k a copy stage: the swizzle's 128 bytes
 constexpr int I8_MAX_STAGES = 6;
 constexpr int I8_MISC = 2048;
@@ -51,6 +54,7 @@ struct I8Args {
   int tn;       // tokens of a tile, a multiple of 16
   int tiles_m;  // token tiles
   int stages;   // of the copy ring
+  int bufs;     // of widened units
   int vec;      // y's rows take 8-byte stores
 };
 
@@ -58,7 +62,7 @@ struct I8Misc {
   float sx[MAX_TN];
   uint32_t tmem;
   int dead;
-  unsigned long long bars[2 * I8_MAX_STAGES + 6];
+  unsigned long long bars[2 * I8_MAX_STAGES + 2 * MAX_BUFS + 1];
 };
 static_assert(sizeof(I8Misc) <= I8_MISC, "misc area");
 
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
   unsigned char* base_p = dyn + (base - smem_addr(dyn));
   I8Misc& sm = *reinterpret_cast<I8Misc*>(base_p);
   const uint32_t xbytes = (uint32_t)a.tn * 128u;         // 128 k of int8, and 64 k of fp16
-  const uint32_t xc = base + I8_MISC, ring = xc + 2 * xbytes;
+  const uint32_t xc = base + I8_MISC, ring = xc + a.bufs * xbytes;
   const uint32_t stage_bytes = TM * 128 + xbytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned split = cluster_size(), rank = cluster_rank();
@@ -124,13 +128,13 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
   auto full = [&](int i) { return bars + 8u * i; };
   auto empty = [&](int i) { return bars + 8u * (I8_MAX_STAGES + i); };
   auto conv_full = [&](int i) { return bars + 8u * (2 * I8_MAX_STAGES + i); };
-  auto conv_empty = [&](int i) { return bars + 8u * (2 * I8_MAX_STAGES + 2 + i); };
-  const uint32_t done = bars + 8u * (2 * I8_MAX_STAGES + 4);
+  auto conv_empty = [&](int i) { return bars + 8u * (2 * I8_MAX_STAGES + MAX_BUFS + i); };
+  const uint32_t done = bars + 8u * (2 * I8_MAX_STAGES + 2 * MAX_BUFS);
   if (threadIdx.x == 0) {
     prefetch_map(&tx);
     prefetch_map(&tw);
     for (int i = 0; i < I8_MAX_STAGES; ++i) bar_init(full(i), 1), bar_init(empty(i), 2 * GROUP);
-    for (int i = 0; i < 2; ++i) bar_init(conv_full(i), GROUP), bar_init(conv_empty(i), 1);
+    for (int i = 0; i < MAX_BUFS; ++i) bar_init(conv_full(i), GROUP), bar_init(conv_empty(i), 1);
     bar_init(done, 1);
     sm.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -142,71 +146,80 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
   volatile int* dead = &sm.dead;
-  auto t_acc = [&](int half) { return tmem + MAX_TN * half; };
-  auto t_a = [&](int buf, int half) { return tmem + 2 * MAX_TN + 64 * buf + 32 * half; };
+  const uint32_t acc_cols = a.bufs == 3 ? MAX_TN3 : MAX_TN;
+  auto t_acc = [&](int half) { return tmem + acc_cols * half; };
+  auto t_a = [&](int buf, int half) { return tmem + 2 * acc_cols + 64 * buf + 32 * half; };
   bool ok = true;
 
-  const int buf = warp >= GROUP ? 1 : 0;         // the group, its half of each stage's k, its buffers
-  const int gw = warp - buf * GROUP;             // the warp in its group
+  const int grp2 = warp >= GROUP ? 1 : 0;        // the group, and its half of each stage's k
+  const int gw = warp - grp2 * GROUP;            // the warp in its group
   if (warp < 2 * GROUP) {
-    // Each unit is read and (W) widened before the wait for its buffer.
+    // Each unit is read and (W) widened before the wait for its buffer: what lies between one unit's MMAs
+    // and the next one's on the same buffer is only the store.  (x widened there too measured slower, 122
+    // against 81 us for 1024 x 7168 x 6284: twice the registers for it.)
     const int row = gw * 32 + lane;              // of the weight tile
     const int e0 = (gw - W_WARPS) * 32 + lane;   // of the x tile's 16-byte chunks, 32 X_WARPS apart
+    int slot = 0, buf = grp2;              // of the ring; of the widened units (2 s + the group, mod bufs)
+    unsigned round = 0, use = 0;           // parities of their uses
+    auto arrive = [&](uint32_t bar) {
+      __syncwarp();
+      if (lane == 0) bar_arrive(bar);
+    };
     for (int s = 0; s < stages; ++s) {
-      const int slot = s % a.stages;
-      if (!(ok = warp_wait(full(slot), (s / a.stages) & 1, dead))) break;
+      if (!(ok = warp_wait(full(slot), round, dead))) break;
       const uint32_t st = ring + slot * stage_bytes;
       if (gw < W_WARPS) {
         uint32_t v[32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 b = lds128(st + swz128(row, 4 * buf + i));
+          const uint4 b = lds128(st + swz128(row, 4 * grp2 + i));
           widen(b.x, v[8 * i], v[8 * i + 1]);
           widen(b.y, v[8 * i + 2], v[8 * i + 3]);
           widen(b.z, v[8 * i + 4], v[8 * i + 5]);
           widen(b.w, v[8 * i + 6], v[8 * i + 7]);
         }
-        if (s > 0 && !(ok = warp_wait(conv_empty(buf), (s & 1) ^ 1, dead))) break;
+        arrive(empty(slot));
+        if (2 * s + grp2 >= a.bufs && !(ok = warp_wait(conv_empty(buf), use ^ 1, dead))) break;
         tc_after();
         tmem_st(t_a(buf, gw >> 2) + ((uint32_t)((gw & 3) * 32) << 16), v);
         tmem_wait_st();
         tc_before();
       } else {
         const uint32_t xs = st + TM * 128, xd = xc + buf * xbytes;
+        // eight rows' chunks at a time: no bank conflicts
+        auto row_of = [](int e) { return (e >> 5) * 8 + (e & 7); };
         uint4 b[X_CHUNKS];
 #pragma unroll
         for (int j = 0; j < X_CHUNKS; ++j) {
           const int e = e0 + 32 * X_WARPS * j;
-          // eight rows' chunks at a time: no bank conflicts
-          if (e < a.tn * 4) b[j] = lds128(xs + swz128((e >> 5) * 8 + (e & 7), 4 * buf + ((e >> 3) & 3)));
+          if (e < a.tn * 4) b[j] = lds128(xs + swz128(row_of(e), 4 * grp2 + ((e >> 3) & 3)));
         }
-        if (s > 0 && !(ok = warp_wait(conv_empty(buf), (s & 1) ^ 1, dead))) break;
+        arrive(empty(slot));
+        if (2 * s + grp2 >= a.bufs && !(ok = warp_wait(conv_empty(buf), use ^ 1, dead))) break;
 #pragma unroll
         for (int j = 0; j < X_CHUNKS; ++j) {
           const int e = e0 + 32 * X_WARPS * j;
           if (e < a.tn * 4) {
-            const int r = (e >> 5) * 8 + (e & 7), i = (e >> 3) & 3;
             uint4 c, d;
             widen(b[j].x, c.x, c.y);
             widen(b[j].y, c.z, c.w);
             widen(b[j].z, d.x, d.y);
             widen(b[j].w, d.z, d.w);
-            sts128(xd + swz128(r, 2 * i), c);
-            sts128(xd + swz128(r, 2 * i + 1), d);
+            sts128(xd + swz128(row_of(e), 2 * ((e >> 3) & 3)), c);
+            sts128(xd + swz128(row_of(e), 2 * ((e >> 3) & 3) + 1), d);
           }
         }
         fence_async();
       }
-      __syncwarp();
-      if (lane == 0) {
-        bar_arrive(conv_full(buf));
-        bar_arrive(empty(slot));
-      }
+      arrive(conv_full(buf));
+      if (++slot == a.stages) slot = 0, round ^= 1;
+      if ((buf += 2) >= a.bufs) buf -= a.bufs, use ^= 1;
     }
   } else if (warp == 2 * GROUP) {  // copies
+    int slot = 0;
+    unsigned round = 1;
     for (int s = 0; s < stages; ++s) {
-      const int slot = s % a.stages;
-      if (s >= a.stages && !(ok = warp_wait(empty(slot), ((s / a.stages) & 1) ^ 1, dead))) break;
+      if (s >= a.stages && !(ok = warp_wait(empty(slot), round, dead))) break;
       if (elect()) {
         const uint32_t st = ring + slot * stage_bytes;
         const int k = (s_begin + s) * KSTAGE;
@@ -215,12 +228,14 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
         tma_load(st + TM * 128, &tx, k, (int)m0, full(slot));
       }
       __syncwarp();
+      if (++slot == a.stages) slot = 0, round ^= 1;
     }
   } else {  // matrix products
     const uint32_t id = idesc_f16(128, a.tn);
+    int buf = 0;
+    unsigned use = 0;
     for (int u = 0; u < 2 * stages; ++u) {  // 64 k each
-      const int buf = u & 1;
-      if (!(ok = warp_wait(conv_full(buf), (u >> 1) & 1, dead))) break;
+      if (!(ok = warp_wait(conv_full(buf), use, dead))) break;
       tc_after();
       if (elect()) {
 #pragma unroll
@@ -233,6 +248,7 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
         if (u + 1 == 2 * stages) mma_commit(done);
       }
       __syncwarp();
+      if (++buf == a.bufs) buf = 0, use ^= 1;
     }
     if (!ok && elect()) mma_commit(done);
   }
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
     if (warp < 2 * GROUP && gw < W_WARPS) {
       const int n = gw * 32 + lane;
       const float sw = n < cols ? a.sw[n0 + n] : 0.0f;
-      for (int c = 16 * buf; c < rows; c += 32) {
+      for (int c = 16 * grp2; c < rows; c += 32) {
         uint32_t v[16];
         tmem_ld(t_acc(gw >> 2) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
         tmem_wait_ld(v);
@@ -287,47 +303,46 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
       }
     }
   } else {
-    constexpr int LD = 132;  // fp32 a row of one half's 128 weight rows
+    constexpr int LD = TM + 4, QUADS = TM / 4;  // fp32 a row; groups of four columns
+    static_assert(I8_MISC + 4 * MAX_TN * LD <= I8_SMEM - 1024, "partial tile");
     float* red = reinterpret_cast<float*>(base_p + I8_MISC);
-    for (int half = 0; half < MH; ++half) {
-      if (warp < 2 * GROUP && gw < W_WARPS && (gw >> 2) == half) {
-        const int n = (gw & 3) * 32 + lane;
-        for (int c = 16 * buf; c < rows; c += 32) {
-          uint32_t v[16];
-          tmem_ld(t_acc(half) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
-          tmem_wait_ld(v);
+    if (warp < 2 * GROUP && gw < W_WARPS) {
+      const int n = gw * 32 + lane;
+      for (int c = 16 * grp2; c < rows; c += 32) {
+        uint32_t v[16];
+        tmem_ld(t_acc(gw >> 2) + ((uint32_t)((warp & 3) * 32) << 16) + c, v);
+        tmem_wait_ld(v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) red[(c + i) * LD + n] = __uint_as_float(v[i]);
-        }
-        tc_before();
+        for (int i = 0; i < 16; ++i) red[(c + i) * LD + n] = __uint_as_float(v[i]);
       }
-      cluster_sync();
-      // this CTA's share: groups of four columns, row by row
-      const int e_end = (int)((long long)rows * 32 * (rank + 1) / split);
-      for (int e = (int)((long long)rows * 32 * rank / split) + threadIdx.x; e < e_end; e += THREADS) {
-        const int r = e >> 5, c = (e & 31) * 4, n = half * 128 + c;
-        if (n >= cols) continue;
-        const uint32_t at = smem_addr(red + r * LD + c);
-        float4 t[MAX_SPLIT];
-#pragma unroll
-        for (int q = 0; q < MAX_SPLIT; ++q)
-          t[q] = (unsigned)q < split ? peer_f32x4(at, q) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 v = t[0];
-#pragma unroll
-        for (int q = 1; q < MAX_SPLIT; ++q) v.x += t[q].x, v.y += t[q].y, v.z += t[q].z, v.w += t[q].w;
-        const float sx = sm.sx[r];
-        const float f[4] = {v.x, v.y, v.z, v.w};
-        __nv_bfloat16* y = a.y + (m0 + r) * a.ldy + n0 + n;
-        if (a.vec && n + 4 <= cols) {
-          const float* sw = a.sw + n0 + n;
-          *reinterpret_cast<uint2*>(y) =
-              make_uint2(pack_bf(f[0] * sx * sw[0], f[1] * sx * sw[1]), pack_bf(f[2] * sx * sw[2], f[3] * sx * sw[3]));
-        } else {
-          for (int i = 0; i < 4 && n + i < cols; ++i) y[i] = __float2bfloat16_rn(f[i] * sx * a.sw[n0 + n + i]);
-        }
-      }
-      cluster_sync();  // the peers have read this CTA's partials
+      tc_before();
     }
+    cluster_sync();
+    // this CTA's share: groups of four columns, row by row
+    const int e_end = (int)((long long)rows * QUADS * (rank + 1) / split);
+    for (int e = (int)((long long)rows * QUADS * rank / split) + threadIdx.x; e < e_end; e += THREADS) {
+      const int r = e / QUADS, n = (e % QUADS) * 4;
+      if (n >= cols) continue;
+      const uint32_t at = smem_addr(red + r * LD + n);
+      float4 t[MAX_SPLIT];
+#pragma unroll
+      for (int q = 0; q < MAX_SPLIT; ++q)
+        t[q] = (unsigned)q < split ? peer_f32x4(at, q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 v = t[0];
+#pragma unroll
+      for (int q = 1; q < MAX_SPLIT; ++q) v.x += t[q].x, v.y += t[q].y, v.z += t[q].z, v.w += t[q].w;
+      const float sx = sm.sx[r];
+      const float f[4] = {v.x, v.y, v.z, v.w};
+      __nv_bfloat16* y = a.y + (m0 + r) * a.ldy + n0 + n;
+      if (a.vec && n + 4 <= cols) {
+        const float* sw = a.sw + n0 + n;
+        *reinterpret_cast<uint2*>(y) =
+            make_uint2(pack_bf(f[0] * sx * sw[0], f[1] * sx * sw[1]), pack_bf(f[2] * sx * sw[2], f[3] * sx * sw[3]));
+      } else {
+        for (int i = 0; i < 4 && n + i < cols; ++i) y[i] = __float2bfloat16_rn(f[i] * sx * a.sw[n0 + n + i]);
+      }
+    }
+    cluster_sync();  // the peers have read this CTA's partials
   }
   __syncthreads();
   if (warp == 2 * GROUP + 1) {
@@ -443,8 +458,10 @@ struct I8Plan {
   double cost = 1e300;
 };
 
+int bufs_of(int tn) { return tn <= MAX_TN3 ? 3 : 2; }
+
 int ring_stages(int mh, int tn) {
-  const int room = I8_SMEM - 1024 - I8_MISC - 2 * tn * 128;
+  const int room = I8_SMEM - 1024 - I8_MISC - bufs_of(tn) * tn * 128;
   const int n = room / ((128 * mh + tn) * 128);
   return n < I8_MAX_STAGES ? n : I8_MAX_STAGES;
 }
@@ -485,10 +502,23 @@ int clusters_held(int dev, int c) {
   return held;
 }
 
-// The launch that the model rates fastest: waves of clusters x (a CTA's 64-k steps + its fixed part).
+// Time model of these tiles, in us, for 1 and 2 halves (fitted to 26 shapes of 17 to 4111 tokens, 256 to 12288 k
+// and 512 to 49376 columns, every TN and C of each, 1200 launches; its pick is within 0.5 % of the
+// fastest on average): a CTA runs its units of 64 k in max(low, base + per_token TN) (base2, per_token2
+// with two buffers), or in its share of what the running CTAs' bytes take at `mb_per_us`, plus a fixed part,
+// plus the split's sum; a last wave costs 1 - tail of a whole one and `tail` by its share.
+struct I8Model {
+  double low[2], base[2], per_token[2], base2[2], per_token2[2], mb_per_us, fixed[2], per_cell, split, split_cell, tail;
+};
+constexpr I8Model I8_MODEL = {{0.296, 0.450},     {0.244, 0.420}, {0.00078, 0.00061}, {0.273, 0.43},
+                              {0.00094, 0.00096}, 18.6,           {4.12, 4.61},       0.0134,
+                              0.75,               0.00607,        0.133};
+
+// The launch that the model rates fastest.
 I8Plan i8_plan(long long M, long long N, long long K, int dev) {
+  constexpr I8Model t = I8_MODEL;
   I8Plan best;
-  const long long steps = (K + 63) / 64, stages = (K + KSTAGE - 1) / KSTAGE;
+  const long long units = (K + 63) / 64, stages = (K + KSTAGE - 1) / KSTAGE;
   for (int mh = 1; mh <= 2; ++mh) {
     const long long tiles_n = (N + 128 * mh - 1) / (128 * mh);
     for (int parts = 0; parts < 8; ++parts) {
@@ -496,14 +526,19 @@ I8Plan i8_plan(long long M, long long N, long long K, int dev) {
       const long long want = (M + MAX_TN - 1) / MAX_TN + parts;
       const int tn = (int)(((M + want - 1) / want + 15) / 16 * 16);
       const long long groups = tiles_n * ((M + tn - 1) / tn);
+      double step = bufs_of(tn) == 3 ? t.base[mh - 1] + t.per_token[mh - 1] * tn
+                                     : t.base2[mh - 1] + t.per_token2[mh - 1] * tn;
+      if (step < t.low[mh - 1]) step = t.low[mh - 1];
+      const double mb = (128.0 * mh + tn) * 64e-6;
       for (int c = 1; c <= MAX_SPLIT && c <= stages; ++c) {
         const int held = mh == 2 ? clusters_held<2>(dev, c) : clusters_held<1>(dev, c);
         if (held <= 0) continue;
-        const double waves = (double)((groups + held - 1) / held);
-        const double mma = 0.021 * tn * mh / 8.0, feed = 0.10 * mh + 0.0006 * tn;
-        const double step = mma > feed ? mma : feed;
+        const double w = (double)groups / held, whole = (double)((groups + held - 1) / held);
+        const double waves = w <= 1.0 ? 1.0 : whole - t.tail * (whole - w);
+        const double running = (double)(groups < held ? groups : held) * c, feed = running * mb / t.mb_per_us;
         const double cost =
-            waves * ((double)steps / c * step + 5.0 + 0.01 * tn * mh + (c > 1 ? 1.5 + 0.01 * tn * mh : 0.0));
+            waves * ((double)units / c * (step > feed ? step : feed) + t.fixed[mh - 1] + t.per_cell * tn * mh +
+                     (c > 1 ? t.split + t.split_cell * tn * mh : 0.0));
         if (cost < best.cost * (1.0 - 1e-9)) best.cost = cost, best.mh = mh, best.tn = tn, best.split = c;
       }
       if (tn <= 16) break;
@@ -523,6 +558,7 @@ int i8_launch(const void* x, long long ldx, const void* w, I8Args a, const I8Pla
   a.tn = p.tn;
   a.tiles_m = (int)((a.M + p.tn - 1) / p.tn);
   a.stages = ring_stages(MH, p.tn);
+  a.bufs = bufs_of(p.tn);
   const long long groups = (a.N + 128 * MH - 1) / (128 * MH) * a.tiles_m;
   if (groups * p.split > 0x7fffffffLL) return KDA_EINVAL;
   cudaLaunchConfig_t cfg;
@@ -558,6 +594,14 @@ extern "C" int kda_linear_i8(const void* x, long long rows, long long ldx, const
   if (rows <= 16) return i8_rows_launch<2, 2, 3>(x, ldx, w, a, st);
   const I8Plan p = i8_plan(rows, N, K, dev);
   if (p.cost >= 1e300) return KDA_ECUDA;
+  // 17 to 32 rows: the fragments kernel where few k make the tiles' fixed part count (32 x 1536 x 7168: 6.1
+  // against 9.8 us; 32 x 7168 x 1154: 13.5 against 10.7).  Its time: a start, and 8 warps' 512 k
+  // at a time, longer as more CTAs share an SM.
+  if (rows <= 32) {
+    const double per_sm = (double)((N + 15) / 16) / sm_count(dev);
+    if (2.5 + (double)((K + 511) / 512) * (0.75 + (per_sm > 1.0 ? 0.26 * (per_sm - 1.0) : 0.0)) < p.cost)
+      return i8_rows_launch<4, 1, 3>(x, ldx, w, a, st);
+  }
   return p.mh == 2 ? i8_launch<2>(x, ldx, w, a, p, st) : i8_launch<1>(x, ldx, w, a, p, st);
 }
 

@@ -149,7 +149,9 @@ def _i8(rows, K, N, seed, lo=-127, hi=127, xpad=0, ypad=0):
     (1, 16, 1), (1, 7168, 1154), (2, 48, 77), (3, 1536, 300), (7, 208, 515), (8, 4096, 256), (9, 272, 129),
     (15, 7168, 100), (16, 1024, 640), (17, 1024, 640), (31, 272, 777), (33, 1536, 512), (64, 1536, 1154), (65, 64, 384),
     (100, 784, 203), (128, 512, 256), (129, 528, 257), (200, 2048, 999), (256, 1536, 384), (300, 272, 640),
-    (513, 144, 1030)])
+    (513, 144, 1030),
+    (18, 256, 500), (32, 512, 3000), (27, 1536, 7168), (161, 256, 40), (176, 1040, 300), (340, 400, 260),
+    (1000, 272, 700)])
 def test_linear_i8(rows, K, N):
     _i8(rows, K, N, seed=rows * 31 + N, xpad=16 * (rows % 3), ypad=rows % 5)
 
