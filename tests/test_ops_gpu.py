@@ -121,6 +121,27 @@ def test_quant_rows_far_magnitudes(size):
     assert ((s.cpu().double() - ws).abs() <= R.scale_bound(512) * ws + 2 * 2.0 ** -149).all()
 
 
+def test_quant_rows_more_rows_than_ctas():
+    # CTAs take rows in turn: the first, ordinary ones, rows that need the careful way, rows that do not, mixed
+    r = _gen(9)
+    x = torch.randn(2500, 256, generator=r)
+    x[::7] *= 1e-38
+    x[1::11] *= 1e25
+    x[5::13] = 0
+    x = x.bfloat16()
+    x[3::401, 17] = float("nan")
+    x[4::403, 250] = float("inf")
+    w = (1 + 0.2 * torch.randn(256, generator=r)).bfloat16()
+    _quant(x, None, None)
+    _quant(x, None, w)
+    res = torch.randn(2500, 256, generator=r).bfloat16()
+    _quant(x, res, w)
+    w[9] = float("nan")
+    _quant(x[:700], None, w)
+    w[9] = float("inf")
+    _quant(x[:700], res[:700], w)
+
+
 def test_quant_rows_none():
     q, s = kda.quant_rows(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV))
     assert q.shape == (0, 64) and s.shape == (0,)
