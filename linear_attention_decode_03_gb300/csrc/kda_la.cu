@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 //
 // What is rounded: P and, as an operand of Q S^T, S to bf16 (an output of bf16
 // anyway).  The state itself is summed from exact parts: K' = hi + mid + lo in bf16 (24
-// bits; hi + mid where the pool is bf16), each chunk's sum added to S in fp32
+// bits; hi + mid where only bf16 comes of it), each chunk's sum added to S in fp32
 // registers, so that nothing accumulates in the tensor pipe over chunks.
 //
 // What bounds it is shared memory's 128 bytes a cycle: a 128 x 128 x 16 MMA takes 8 KB of
@@ -195,9 +195,11 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 //   MMA:     QK QS | mid, hi | lo PV                | QK ...
 //   compute: scores -> P; QS * e^G | K -> K' of the next chunk | S += K'^T V | outputs
 //
-// A long sequence is split into segments to fill the GPU: la_chunk_kernel<., true> computes
-// each segment's own contribution to the state, la_join_kernel turns these into the states the
-// segments start from, and la_chunk_kernel<., false> runs all segments at once.
+// A long sequence is split into segments to fill the GPU: la_chunk_kernel<OWN> computes each
+// segment's own contribution to the state, la_join_kernel turns these into the states the segments
+// start from and the one behind the last, and la_chunk_kernel<OUTPUT> runs all segments at once for their
+// outputs (its states end as bf16 operands, so hi and mid will do).  Where no sequence needs that,
+// la_chunk_kernel<DIRECT> does all of it in one launch.
 constexpr int CHUNK = 128;
 constexpr int BOX = 64 * 128 * 2;          // 64 columns of 128 rows, bf16
 constexpr int TILE = 2 * BOX;              // a 128 x 128 bf16 operand
@@ -295,7 +297,7 @@ struct ChunkMisc {
   float W[CHUNK];  // e^{R_j}, used up to the sequence's end
   float E[CHUNK];  // e^{G_b - G_j}, G_b the last G of j's block of 16
   float total;     // G_C (log2)
-  int found, dead;
+  int found, dead, slot, resumed;
   uint32_t tmem;
   long long number;
   Segment seg;
@@ -303,11 +305,15 @@ struct ChunkMisc {
 };
 static_assert(sizeof(ChunkMisc) <= MISC, "misc area");
 
-template <bool BF, bool LOCAL>
+enum Mode { DIRECT, OWN, OUTPUT };
+
+// BF: a bf16 pool (DIRECT; the other two read and write the workspace's fp32 only)
+template <Mode MODE, bool BF>
 __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     la_chunk_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                     const ChunkArgs p) {
+  constexpr bool LOCAL = MODE == OWN, LO = MODE == OWN || (MODE == DIRECT && !BF);  // with the third part of K'
   const LaArgs& a = p.a;
   extern __shared__ __align__(1024) unsigned char dyn[];
   // (all shared memory is dynamic: the seven operand tiles leave no room for a second alignment)
@@ -316,11 +322,21 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   ChunkMisc& sm = *reinterpret_cast<ChunkMisc*>(dyn + (base - smem_addr(dyn)) + 7 * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = (int)(blockIdx.x % a.heads), hk = h / a.share;
+  const uint32_t bars = smem_addr(sm.bars);
+  auto bar = [&](int i) { return bars + 8u * i; };
+  // which segment, the barriers and the tensor memory, each by a warp, then one barrier
   if (warp == 0) {
     Segment s;
     long long number = 0;
-    const bool found = find_segment(a, p.m, p.segments, blockIdx.x / a.heads, false, &s, &number);
-    if (lane == 0) sm.seg = s, sm.number = number, sm.found = found, sm.dead = 0;
+    bool found = find_segment(a, p.m, p.segments, blockIdx.x / a.heads, false, &s, &number);
+    if (lane == 0) {
+      sm.found = found, sm.dead = 0;
+      if (found) {
+        sm.seg = s, sm.number = number;
+        sm.slot = a.slots[s.seq];
+        sm.resumed = MODE == OUTPUT || (MODE == DIRECT && a.has_state && a.has_state[s.seq]);
+      }
+    }
     if (!LOCAL && blockIdx.x == 0) {  // bad pairs of cu_seqlens are reported once
       bool bad = false;
       long long all = 0;
@@ -335,57 +351,57 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
       if (bad || all > p.segments) atomicOr(&g_la_err, KDA_ERR_SEQ);
     }
-  }
-  __syncthreads();
-  if (!sm.found) return;
-  const Segment sg = sm.seg;
-  const long long number = sm.number;
-  const bool last_seg = sg.index == sg.count - 1;
-  const int slot = a.slots[sg.seq];
-  const long long row0 = sg.begin + (long long)sg.index * p.m * CHUNK;
-  const long long left = sg.end - row0;
-  const int tokens = (int)(left < (long long)p.m * CHUNK ? left : (long long)p.m * CHUNK);
-  const int chunks = (tokens + CHUNK - 1) / CHUNK;
-  if (slot < 0 || slot >= a.pool) {
-    if (!LOCAL && slot == -1) {
-      for (int e = threadIdx.x; e < tokens * (D / 8); e += CHUNK_THREADS)
-        *reinterpret_cast<uint4*>(a.out + (row0 + e / (D / 8)) * a.ldo + h * D + 8 * (e % (D / 8))) =
-            make_uint4(0, 0, 0, 0);
-    } else if (!LOCAL && threadIdx.x == 0) {
-      atomicOr(&g_la_err, KDA_ERR_SLOT);
+  } else if (warp == COMPUTE_WARPS) {
+    if (lane == 0) {
+      for (int i = 0; i < BARS; ++i)
+        bar_init(bar(i), i >= QUARTER                         ? 4
+                         : i == EMPTY_K || i == EMPTY_K + 1 ? COMPUTE_WARPS + (LOCAL ? 0 : 1)
+                         : i >= EMPTY_Q                     ? COMPUTE_WARPS
+                                                            : 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      if (!LOCAL) prefetch_map(&tq), prefetch_map(&to);
+      prefetch_map(&tk);
+      prefetch_map(&tv);
     }
-    return;
+  } else if (warp == COMPUTE_WARPS + 1) {
+    tmem_alloc(smem_addr(&sm.tmem), 512);
   }
-  if (LOCAL && last_seg) return;  // nobody starts from its state
-  const bool resumed = !LOCAL && (sg.count > 1 || (a.has_state && a.has_state[sg.seq]));  // starts from a state
-  unsigned char* pool = static_cast<unsigned char*>(a.state) + ((long long)slot * a.heads + h) * (D * D) * (BF ? 2 : 4);
-  float* wsp = p.ws + (number * a.heads + h) * (D * D);
-  if (!LOCAL && chunks == 0) {  // an empty sequence: its state stays, or is zeros
-    if (!resumed)
-      for (int e = threadIdx.x; e < D * D * (BF ? 2 : 4) / 16; e += CHUNK_THREADS)
-        reinterpret_cast<uint4*>(pool)[e] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-
-  const uint32_t bars = smem_addr(sm.bars);
-  auto bar = [&](int i) { return bars + 8u * i; };
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < BARS; ++i)
-      bar_init(bar(i), i >= QUARTER                                  ? 4
-                       : i == EMPTY_K || i == EMPTY_K + 1 ? COMPUTE_WARPS + (LOCAL ? 0 : 1)
-                       : i >= EMPTY_Q                     ? COMPUTE_WARPS
-                                                          : 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (!LOCAL) prefetch_map(&tq), prefetch_map(&to);
-    prefetch_map(&tk);
-    prefetch_map(&tv);
-  }
-  if (warp == COMPUTE_WARPS + 1) tmem_alloc(smem_addr(&sm.tmem), 512);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
   if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // A CTA without work: no segment, a padding sequence (its rows zero), a bad slot, an empty sequence (its
+  // state stays, or is zeros; the join's where there is one).
+  const Segment sg = sm.seg;
+  const long long number = sm.number;
+  const int slot = sm.slot;
+  const bool resumed = sm.resumed;  // starts from a state
+  const long long row0 = sg.begin + (long long)sg.index * p.m * CHUNK;
+  const long long left = sg.end - row0;
+  const int tokens = (int)(left < (long long)p.m * CHUNK ? left : (long long)p.m * CHUNK);
+  const int chunks = (tokens + CHUNK - 1) / CHUNK;
+  const bool slot_ok = slot >= 0 && slot < a.pool;
+  unsigned char* pool = static_cast<unsigned char*>(a.state) + ((long long)slot * a.heads + h) * (D * D) * (BF ? 2 : 4);
+  if (!sm.found || !slot_ok || chunks == 0) {
+    if (sm.found && !LOCAL) {
+      if (slot == -1) {
+        for (int e = threadIdx.x; e < tokens * (D / 8); e += CHUNK_THREADS)
+          *reinterpret_cast<uint4*>(a.out + (row0 + e / (D / 8)) * a.ldo + h * D + 8 * (e % (D / 8))) =
+              make_uint4(0, 0, 0, 0);
+      } else if (!slot_ok) {
+        if (threadIdx.x == 0) atomicOr(&g_la_err, KDA_ERR_SLOT);
+      } else if (MODE == DIRECT && !resumed) {
+        for (int e = threadIdx.x; e < D * D * (BF ? 2 : 4) / 16; e += CHUNK_THREADS)
+          reinterpret_cast<uint4*>(pool)[e] = make_uint4(0, 0, 0, 0);
+      }
+    }
+    if (warp == COMPUTE_WARPS + 1) tmem_free(tmem, 512);
+    // (a kernel behind this one waits for this one alone: it ends after the one before it)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  float* wsp = p.ws + (number * a.heads + h) * (D * D);
   // tensor memory: scores, then P and lo; hi and mid; outputs; K'^T V.  (LOCAL: two sets of hi, mid, lo; K'^T V)
   const uint32_t t_sc = tmem, t_p = tmem, t_o = tmem + 256, t_ds = tmem + 384;
   auto t_hi = [&](int c) { return LOCAL ? tmem + 192 * (c & 1) : tmem + 128; };
@@ -396,8 +412,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   auto sv = [&](int c) { return sq(c) + 2 * TILE; };
   volatile int* dead = &sm.dead;
   auto wait = [&](int i, unsigned ph) { return warp_wait(bar(i), ph, dead); };  // whole warps only
-  // the state behind the segment's last chunk is wanted: by the pool, or (LOCAL) by the join
-  const bool want_last = LOCAL || last_seg;
+  // the state behind the segment's last chunk is wanted: by the pool, or (OWN) by the join
+  constexpr bool want_last = MODE != OUTPUT;
   bool ok = true;
 
   if (warp < COMPUTE_WARPS) {
@@ -417,12 +433,12 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     float S[32];  // S[v = c0 ..][k = r]
     if (resumed) {
       const long long at = (long long)c0 * D + r;
-      if (BF && sg.count == 1) {
+      if (MODE == DIRECT && BF) {
         const uint16_t* f = reinterpret_cast<const uint16_t*>(pool) + at;
 #pragma unroll
         for (int i = 0; i < 32; ++i) S[i] = __uint_as_float((uint32_t)f[i * D] << 16);
       } else {
-        const float* f = reinterpret_cast<const float*>(sg.count > 1 ? reinterpret_cast<unsigned char*>(wsp) : pool) + at;
+        const float* f = reinterpret_cast<const float*>(MODE == OUTPUT ? reinterpret_cast<unsigned char*>(wsp) : pool) + at;
 #pragma unroll
         for (int i = 0; i < 32; ++i) S[i] = __ldcg(f + i * D);
       }
@@ -475,7 +491,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
                 float f0 = bf_lo(x) * w.x, f1 = bf_hi(x) * w.y;
                 hi[o] = top_halves(f0, f1);
                 f0 -= bf_cut(f0), f1 -= bf_cut(f1);
-                if (BF) {
+                if (!LO) {
                   mid[o] = pack_bf(f0, f1);
                 } else {
                   mid[o] = top_halves(f0, f1);
@@ -554,7 +570,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         if (!(ok = wait(QUARTER + quarter, ph))) break;
         tc_after();
         tmem_st(t_p + lane_at + c0 / 2, pk);
-        if (!BF && wanted(c)) {
+        if (LO && wanted(c)) {
           tmem_st_frag(t_lo(c) + lane_at + c0 / 2, lo[0]);
           tmem_st_frag(t_lo(c) + lane_at + (16u << 16) + c0 / 2, lo[1]);
         }
@@ -640,7 +656,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     if (!LOCAL && lane == 0) tma_store_read();  // before the memory goes
     if (ok && want_last) {
       const long long at = (long long)c0 * D + r;
-      if (BF) {
+      if (MODE == DIRECT && BF) {
         __nv_bfloat16* f = reinterpret_cast<__nv_bfloat16*>(pool) + at;
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i * D] = __float2bfloat16_rn(S[i]);
@@ -763,7 +779,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         tc_after();
         if (elect()) {
           if (want) {
-            if (!BF) delta(t_lo(c), false);
+            if (LO) delta(t_lo(c), false);
             mma_commit(bar(DELTA));
           }
 #pragma unroll
@@ -799,7 +815,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 }
 
 // From the segments' own states to the states they start from, elementwise and in place in
-// the workspace: four values a thread, JOIN_PARTS CTAs a state, the loads of JOIN_AHEAD segments
+// the workspace, and to the one behind the last segment, in the pool: four values a thread, JOIN_PARTS CTAs a state, the loads of JOIN_AHEAD segments
 // in flight together.
 constexpr int JOIN_PARTS = 16, JOIN_AHEAD = 8;
 template <bool BF>
@@ -812,10 +828,6 @@ __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
   const long long task = blockIdx.x / JOIN_PARTS;
   const long long seq = task / a.heads;
   const int h = (int)(task % a.heads);
-  {
-    const long long b = a.cu[seq], e = a.cu[seq + 1];
-    if (!seq_ok(a, b, e) || seg_count(e - b, p.m) < 2) return;
-  }
   if (threadIdx.x < 32) {
     Segment s;
     long long number = 0;
@@ -823,14 +835,16 @@ __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
     if (threadIdx.x == 0) s_seg = s, s_number = number, s_found = found;
   }
   __syncthreads();
-  if (!s_found) return;
   const int slot = a.slots[seq];
-  if (slot < 0 || slot >= a.pool) return;
-  const int count = s_seg.count;
+  if (!s_found || slot < 0 || slot >= a.pool) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const int count = s_seg.end > s_seg.begin ? s_seg.count : 0;  // (without tokens the state is the start's)
   const int at = (int)(blockIdx.x % JOIN_PARTS) * (D * D / JOIN_PARTS) + 4 * threadIdx.x;
+  const long long e = ((long long)slot * a.heads + h) * (D * D) + at;
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.has_state && a.has_state[seq]) {
-    const long long e = ((long long)slot * a.heads + h) * (D * D) + at;
     if (BF) {
       const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.state) + e);
       S = make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
@@ -840,25 +854,29 @@ __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
   }
   const long long step = (long long)a.heads * (D * D / 4);
   float4* w = reinterpret_cast<float4*>(p.ws + (s_number * a.heads + h) * (D * D) + at);
-  const float* d = p.decays + s_number * a.heads + h;
+  const float* decays = p.decays + s_number * a.heads + h;
   // the segments' states are the kernel before's
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int s0 = 0; s0 < count; s0 += JOIN_AHEAD, w += JOIN_AHEAD * step, d += (long long)JOIN_AHEAD * a.heads) {
+  for (int s0 = 0; s0 < count; s0 += JOIN_AHEAD, w += JOIN_AHEAD * step, decays += (long long)JOIN_AHEAD * a.heads) {
     float4 own[JOIN_AHEAD];
     float f[JOIN_AHEAD];
 #pragma unroll
-    for (int i = 0; i < JOIN_AHEAD; ++i) {  // (the last segment's own state is nobody's start)
-      const bool more = s0 + i + 1 < count;
+    for (int i = 0; i < JOIN_AHEAD; ++i) {
+      const bool more = s0 + i < count;
       own[i] = more ? __ldcg(w + i * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-      f[i] = more ? __ldcg(d + (long long)i * a.heads) : 0.0f;
+      f[i] = more ? __ldcg(decays + (long long)i * a.heads) : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < JOIN_AHEAD; ++i) {
       if (s0 + i < count) w[i * step] = S;
-      const float e = ex2(f[i]);
-      S = make_float4(fmaf(e, S.x, own[i].x), fmaf(e, S.y, own[i].y), fmaf(e, S.z, own[i].z), fmaf(e, S.w, own[i].w));
+      const float d = ex2(f[i]);  // (1 behind the last)
+      S = make_float4(fmaf(d, S.x, own[i].x), fmaf(d, S.y, own[i].y), fmaf(d, S.z, own[i].z), fmaf(d, S.w, own[i].w));
     }
   }
+  if (BF)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.state) + e) = make_uint2(pack_bf(S.x, S.y), pack_bf(S.z, S.w));
+  else
+    *reinterpret_cast<float4*>(static_cast<float*>(a.state) + e) = S;
 }
 
 // The checks that step and prefill share.  Without rows (a prompt call of empty
@@ -972,31 +990,31 @@ int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   cfg.dynamicSmemBytes = CHUNK_SMEM;
   cfg.stream = st;
   // the shared-memory attribute is per device and cheap: set on every call
-  if (cudaFuncSetAttribute(la_chunk_kernel<BF, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
-      cudaSuccess)
-    return KDA_ECUDA;
-  if (cut.split) {
-    // (the workspace is fp32 whatever the pool)
-    if (cudaFuncSetAttribute(la_chunk_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) !=
-            cudaSuccess ||
-        cudaLaunchKernelEx(&cfg, la_chunk_kernel<false, true>, tq, tk, tv, to, p) != cudaSuccess)
+  auto big = [](auto* kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) == cudaSuccess;
+  };
+  if (!cut.split) {
+    if (!big(la_chunk_kernel<DIRECT, BF>) ||
+        cudaLaunchKernelEx(&cfg, la_chunk_kernel<DIRECT, BF>, tq, tk, tv, to, p) != cudaSuccess)
       return KDA_ECUDA;
-    // the two kernels behind it may start while the one before ends, and wait where they read its results
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchConfig_t join = cfg;
-    join.gridDim = dim3((unsigned)(p.a.seqs * p.a.heads * JOIN_PARTS), 1, 1);
-    join.blockDim = dim3(256, 1, 1);
-    join.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&join, la_join_kernel<BF>, p) != cudaSuccess ||
-        cudaLaunchKernelEx(&cfg, la_chunk_kernel<BF, false>, tq, tk, tv, to, p) != cudaSuccess)
-      return KDA_ECUDA;
-  } else if (cudaLaunchKernelEx(&cfg, la_chunk_kernel<BF, false>, tq, tk, tv, to, p) != cudaSuccess) {
-    return KDA_ECUDA;
+    return launched();
   }
+  if (!big(la_chunk_kernel<OWN, false>) || !big(la_chunk_kernel<OUTPUT, false>) ||
+      cudaLaunchKernelEx(&cfg, la_chunk_kernel<OWN, false>, tq, tk, tv, to, p) != cudaSuccess)
+    return KDA_ECUDA;
+  // the two kernels behind it may start while the one before ends, and wait where they read its results
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchConfig_t join = cfg;
+  join.gridDim = dim3((unsigned)(p.a.seqs * p.a.heads * JOIN_PARTS), 1, 1);
+  join.blockDim = dim3(256, 1, 1);
+  join.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&join, la_join_kernel<BF>, p) != cudaSuccess ||
+      cudaLaunchKernelEx(&cfg, la_chunk_kernel<OUTPUT, false>, tq, tk, tv, to, p) != cudaSuccess)
+    return KDA_ECUDA;
   return launched();
 }
 
