@@ -945,12 +945,14 @@ struct Cut {
   bool split;  // some sequence may have several segments
 };
 
-// Times in us: a chunk of a segment, a segment's fixed part; the same for the pass over
-// the segments' own states; the join.
-constexpr double T_CHUNK = 1.9, T_FIXED = 5.0, T_OWN = 1.3, T_OWN_FIXED = 5.0, T_JOIN = 4.0;
+// Time model in us (fitted to 16 shapes, 128 to 16384 rows of 1 to 96 heads, each at 3 to 14 values of m): a chunk
+// and a CTA's start without a split; with one a chunk in both passes, the three kernels' start, another
+// wave, a segment's states through the join.
+constexpr double T_CHUNK = 3.26, T_START = 5.5, T_CHUNK2 = 4.06, T_START2 = 10.0, T_WAVE2 = 5.0, T_JOIN2 = 0.085;
 
 Cut la_cut(long long rows, int heads, long long seqs, long long max_len, int sms) {
-  const long long longest = (max_len < rows ? max_len : rows) / CHUNK + 1;  // chunks, about
+  long long longest = ((max_len < rows ? max_len : rows) + CHUNK - 1) / CHUNK;  // chunks
+  if (longest < 1) longest = 1;
   const double chunks = (double)rows / CHUNK + 0.5 * (double)seqs;
   Cut best = {};
   double least = 1e300;
@@ -962,8 +964,8 @@ Cut la_cut(long long rows, int heads, long long seqs, long long max_len, int sms
     const double w = segs * heads / sms;
     const double waves = w <= 1.0 ? 1.0 : (double)(long long)(w + 0.999);
     const double run = per * waves > (double)m ? per * waves : (double)m;
-    double t = run * T_CHUNK + waves * T_FIXED;
-    if (!last) t += run * T_OWN + waves * T_OWN_FIXED + T_JOIN;
+    const double t = last ? run * T_CHUNK + waves * T_START
+                          : run * T_CHUNK2 + T_START2 + (waves - 1.0) * T_WAVE2 + segs * heads * T_JOIN2;
     if (t < least * 0.999) {
       least = t;
       best.m = (int)(m > 0x1000000 ? 0x1000000 : m);
