@@ -200,13 +200,15 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
     block_reduce(top_bits, sum, s_top[turn], s_sum[turn]);
     top = __uint_as_float(top_bits);
     float scale, inv;
-    if (top >= 0x1p-100f && top_bits < 0x7f800000u && (!NORM || sum <= 0x1p120f)) {
+    if (top >= 0x1p-100f && top < 0x1p119f && (!NORM || (sum <= 0x1p120f && (sum >= 0x1p-80f || a.eps >= 0x1p-60f)))) {
       scale = (NORM ? 1.0f / sqrtf(sum / (float)a.cols + a.eps) : 1.0f) * (top / 127.0f);
       inv = 127.0f / top;
     } else {
       // The careful way, for rows of zeros, with values that are not finite, or whose products or squares leave
-      // fp32's range: once more with h (and w) times a power of two.
-      const float up = top < 0x1p-100f ? 0x1p64f : 1.0f, down = NORM && sum > 0x1p120f ? 0x1p-80f : 1.0f;
+      // fp32's range: once more with h (and w) times a power of two for p, and h times another for the sum.  Whatever that
+      // pushes out of range is too small to count.
+      const float up = top < 0x1p-100f ? 0x1p90f : top >= 0x1p119f ? 0x1p-72f : 1.0f;
+      const float down = !NORM ? 1.0f : sum > 0x1p120f ? 0x1p-80f : sum < 0x1p-80f && a.eps < 0x1p-60f ? 0x1p90f : 1.0f;
       top_bits = 0, sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -215,7 +217,8 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
         load_w(i, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          p[i][j] = NORM ? (h[j] * up) * (w[j] * up) : h[j] * up;
+          // (a zero times anything finite stays one, whatever the other's size)
+          p[i][j] = !NORM ? h[j] * up : h[j] == 0.0f || w[j] == 0.0f ? h[j] * w[j] : (h[j] * up) * (w[j] * up);
           top_bits = max(top_bits, __float_as_uint(fabsf(p[i][j])));
           sum = fmaf(h[j] * down, h[j] * down, sum);
         }
@@ -229,8 +232,8 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
         scale = 0.0f;
       } else {
         const float unit = 1.0f / up;
-        scale = (NORM ? down / sqrtf(sum / (float)a.cols + a.eps * down * down) : 1.0f) * (top / 127.0f) * unit;
-        if (NORM) scale *= unit;
+        scale = (top / 127.0f) * unit;
+        if (NORM) scale = (top / 127.0f) / sqrtf(sum / (float)a.cols + a.eps * down * down) * (down * unit) * unit;
         inv = 127.0f / top;
       }
     }

@@ -121,6 +121,46 @@ def test_quant_rows_far_magnitudes(size):
     assert ((s.cpu().double() - ws).abs() <= R.scale_bound(512) * ws + 2 * 2.0 ** -149).all()
 
 
+@pytest.mark.parametrize("h,w,eps", [
+    (1e-25, 1.0, 0.0), (1e-38, 1.0, 0.0), (1e-25, 1e10, 0.0), (1e-25, 1e10, 1e-30), (1e-12, 1.0, 1e-25),  # squares too small
+    (1e-38, 1e-37, 0.0), (1e-30, 1e-20, 1e-6), (1e-38, 1e-38, 1e-4),  # products too small
+    (1e30, 1e30, 1e-6), (1e37, 1e5, 1e-6), (1e2, 1e37, 1e-6), (2e38, 1.0, 1e-6)])  # products or squares too large
+def test_quant_rows_products_out_of_range(h, w, eps):
+    r = _gen(10)
+    x = (torch.randint(-254, 255, (20, 512), generator=r) / 254 * h).bfloat16()
+    x[:, 0] = torch.tensor(h).bfloat16()
+    weight = (torch.ones(512) * w).bfloat16()
+    cases = [weight, (weight * (0.5 + 0.5 * torch.rand(512, generator=r))).bfloat16()]
+    cases.append(cases[1].clone())
+    cases[2][1::2] = 0  # zeros next to a large or a scaled factor
+    for c in cases:
+        wq, ws, _ = R.quant_rows(x, None, c, eps)
+        q, s = kda.quant_rows(x.to(DEV), norm_weight=c.to(DEV), eps=eps)
+        assert torch.equal(q.cpu().long(), wq)
+        # a scale below fp32's normal range is rounded to its steps, at most twice
+        assert ((s.cpu().double() - ws).abs() <= R.scale_bound(512) * ws + 2 * 2.0 ** -149).all()
+
+
+def test_quant_rows_zeros_next_to_the_largest():
+    big = torch.tensor(3.3e38).bfloat16()
+    x, w = torch.zeros(3, 64).bfloat16(), torch.zeros(64).bfloat16()
+    x[1, 3], x[2] = big, 1e-35
+    w[5], w[8] = big, 1e-20
+    q, s = kda.quant_rows(x.to(DEV), norm_weight=w.to(DEV))
+    wq, ws, _ = R.quant_rows(x, None, w, 1e-6)
+    assert torch.equal(q.cpu().long(), wq) and (s[:2] == 0).all()
+    assert abs(float(s[2]) - float(ws[2])) <= R.scale_bound(64) * float(ws[2])
+
+
+@pytest.mark.parametrize("size", [1e36, 3e36, 1e38, 3.3e38])
+def test_quant_rows_largest_on_halves(size):
+    r = _gen(12)
+    x = torch.randint(-254, 255, (200, 512), generator=r).float() * 2.0 ** 111
+    x[:, 0] = 254 * 2.0 ** 111
+    k = 2.0 ** int(torch.tensor(size).log2().floor() - 119)
+    _quant((x * k).bfloat16(), None, None)
+
+
 def test_quant_rows_more_rows_than_ctas():
     # CTAs take rows in turn: the first, ordinary ones, rows that need the careful way, rows that do not, mixed
     r = _gen(9)
