@@ -5,7 +5,8 @@ head, one token at a time (:func:`la_step`) and over prompts
 arguments; everything runs in the kernels of ``libkda.so``.
 
 Each takes CUDA tensors of one device, which need not be the current one, and
-enqueues on that device's current stream, or on ``stream`` (a raw handle).
+enqueues on that device's current stream, or on ``stream`` (a raw handle), which
+then owns the results that are not given: use them there, or on streams that wait for it.
 """
 from __future__ import annotations
 
@@ -31,6 +32,14 @@ def _call(name, device, stream, *args):
             rc = fn(*args, stream or None)
     if rc != 0:
         raise KdaError(name, rc)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on `stream` writes: owned by that stream, so that it was not handed on too early."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _check(name, stream, device):
@@ -109,10 +118,10 @@ def quant_rows(x, residual=None, norm_weight=None, *, eps: float = 1e-6, out=Non
         _vector(norm_weight, "norm_weight", _BF16, device, cols)
         weight = norm_weight.data_ptr()
     if out is None:
-        out = torch.empty(shape, dtype=_I8, device=device)
+        out = _empty(shape, _I8, device, stream)
     ldq = _matrix(out, "out", _I8, device, shape)
     if scales is None:
-        scales = torch.empty((rows,), dtype=_F32, device=device)
+        scales = _empty((rows,), _F32, device, stream)
     _vector(scales, "scales", _F32, device, rows)
     _call("kda_quant_rows", device, stream, x.data_ptr(), rows, ldx, cols, res, ldr, weight, eps, out.data_ptr(), ldq,
           scales.data_ptr())
@@ -132,7 +141,7 @@ def linear_i8(x, x_scales, w, w_scales, out=None, *, stream=None):
     _vector(x_scales, "x_scales", _F32, device, rows)
     _vector(w_scales, "w_scales", _F32, device, N)
     if out is None:
-        out = torch.empty((rows, N), dtype=_BF16, device=device)
+        out = _empty((rows, N), _BF16, device, stream)
     ldy = _matrix(out, "out", _BF16, device, (rows, N))
     _call("kda_linear_i8", device, stream, x.data_ptr(), rows, ldx, x_scales.data_ptr(), w.data_ptr(),
           w_scales.data_ptr(), N, K, out.data_ptr(), ldy)
@@ -149,7 +158,7 @@ def _heads(t, name, rows, device):
     _refuse(t, name, _BF16, device, f"[{rows}, heads, {HEAD_DIM}]", "with strides [row, 128, 1]")
 
 
-def _attention(q, k, v, g, state, slots, scale, out):
+def _attention(q, k, v, g, state, slots, scale, out, stream):
     """The arguments that step and prompt share, checked."""
     device = _cuda(v, "v", _BF16)
     rows = v.shape[0]
@@ -176,7 +185,7 @@ def _attention(q, k, v, g, state, slots, scale, out):
             and slots.is_contiguous()):
         _refuse(slots, "slots", _I32, device, "[slots]", "and contiguous")
     if out is None:
-        out = torch.empty((rows, heads, HEAD_DIM), dtype=_BF16, device=device)
+        out = _empty((rows, heads, HEAD_DIM), _BF16, device, stream)
     out_heads, ldo = _heads(out, "out", rows, device)
     if out_heads != heads:
         raise ValueError("out must be v's [rows, heads, 128]")
@@ -194,7 +203,7 @@ def la_step(q, k, v, g, *, state, slots, scale=None, out=None, stream=None):
     row will do), g fp32 [heads] or [rows, heads] (log decays, <= 0), state
     [pool, heads, 128 (v), 128 (k)] fp32 or bf16, slots int32 [>= rows] (-1: a padding
     row).  ``scale`` is 128 ** -0.5 unless given.  Returns out [rows, heads, 128]."""
-    device, rows, _, pool, args, out, ldo = _attention(q, k, v, g, state, slots, scale, out)
+    device, rows, _, pool, args, out, ldo = _attention(q, k, v, g, state, slots, scale, out, stream)
     if slots.shape[0] < rows:
         raise ValueError("slots needs an entry for each row")
     _call("kda_la_step", device, stream, *args, state.data_ptr(), _STATE[state.dtype], pool, slots.data_ptr(),
@@ -214,7 +223,7 @@ def la_prefill(q, k, v, g, *, state, slots, cu_seqlens, max_len, has_state=None,
     ``workspace`` (uint8, ``la_prefill_workspace`` bytes) is made if not given.
     The other arguments are as in :func:`la_step`, slots by sequence.  Rows of
     ``out`` behind the last sequence are left as they are."""
-    device, rows, heads, pool, args, out, ldo = _attention(q, k, v, g, state, slots, scale, out)
+    device, rows, heads, pool, args, out, ldo = _attention(q, k, v, g, state, slots, scale, out, stream)
     if not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dtype == _I32 and cu_seqlens.device == device
             and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] > 0 and cu_seqlens.is_contiguous()):
         _refuse(cu_seqlens, "cu_seqlens", _I32, device, "[seqs + 1]", "and contiguous")
@@ -234,11 +243,7 @@ def la_prefill(q, k, v, g, *, state, slots, cu_seqlens, max_len, has_state=None,
                 and workspace.is_contiguous() and workspace.numel() >= need):
             _refuse(workspace, "workspace", torch.uint8, device, f"[>= {need}]", "and contiguous")
     elif need:
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:  # owned by the stream that uses it, so that its memory is not handed on too early
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = _empty(need, torch.uint8, device, stream)
     _call("kda_la_prefill", device, stream, *args, cu_seqlens.data_ptr(), seqs, max_len, has, state.data_ptr(),
           _STATE[state.dtype], pool, slots.data_ptr(), out.data_ptr(), ldo,
           workspace.data_ptr() if workspace is not None else None,

@@ -211,6 +211,47 @@ def test_an_explicit_stream():
     del junk
 
 
+def test_results_of_an_explicit_stream():
+    """stream= without out: the results are that stream's memory, not blocks that the current stream has freed with
+    writes still to come."""
+    r = torch.Generator().manual_seed(70)
+    x = torch.randn(64, 1024, generator=r).bfloat16().to(DEV)
+    w = torch.randint(-127, 128, (512, 1024), generator=r).to(torch.int8).to(DEV)
+    sw = torch.rand(512, generator=r).to(DEV)
+    q8, sx = kda.quant_rows(x)
+    y = kda.linear_i8(q8, sx, w, sw)
+    qkv = torch.randn(3, 64, 2, 128, generator=r).bfloat16().to(DEV)
+    g = -torch.rand(2, generator=r).to(DEV)
+    slots = torch.arange(64, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 64], dtype=torch.int32, device=DEV)
+
+    def state():
+        return torch.zeros(64, 2, 128, 128, device=DEV)
+
+    calls = [lambda s: kda.quant_rows(x, stream=s), lambda s: (kda.linear_i8(q8, sx, w, sw, stream=s),),
+             lambda s: (kda.la_step(*qkv, g, state=states[0], slots=slots, stream=s),),
+             lambda s: (kda.la_prefill(*qkv, g, state=states[1], slots=slots, cu_seqlens=cu, max_len=64, stream=s),)]
+    states = [state(), state()]
+    want = [[t.clone() for t in c(None)] for c in calls]
+    assert torch.equal(want[0][0], q8) and torch.equal(want[1][0], y)
+    side = torch.cuda.Stream()
+    for s in (side.cuda_stream, 0):
+        states = [state(), state()]
+        torch.cuda.synchronize()
+        for call, expect in zip(calls, want):
+            kept = [torch.empty_like(t) for t in expect]  # a block of each size that the call would be given
+            torch.cuda.synchronize()
+            with torch.cuda.stream(torch.cuda.default_stream()):
+                torch.cuda._sleep(10_000_000)
+            for t in kept:
+                t.view(torch.uint8).fill_(99)
+            del kept, t
+            got = call(s)
+            torch.cuda.synchronize()
+            for a, b in zip(got, expect):
+                assert torch.equal(a, b)
+
+
 def test_captured_and_replayed():
     """The layer in a CUDA graph, replayed on new inputs, equals the calls made one by one; two graphs with
     segments each have a workspace of their own."""
