@@ -16,7 +16,9 @@
 // way into shared memory meanwhile (asynchronous 16-byte copies; each thread reads back its own, so
 // they need no barrier).  8191 x 7168 with norm and residual: 411 MB in 64 us, 0.94 of the measured copy
 // bandwidth (a CTA a row, without the copies ahead: 87 us); 4 vectors a thread in 224 threads against 2 in 448: 64
-// and 84 us; a ring of three rows and fewer registers for more CTAs were no faster.
+// and 84 us; a ring of three rows 73 us.  With fewer bytes a value the instructions count too: products, squares and
+// roundings two at a time (f32x2), and without a norm the row stays packed and its maximum is
+// taken on bf16 bit patterns (51 registers instead of 59: three CTAs an SM), 1024 x 12288 12.9 -> 11.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -41,6 +43,40 @@ struct QuantArgs {
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Two floats in a register pair, for the instructions that work on two at a time.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F2 bf2(uint32_t u) { return pack2(bf_lo(u), bf_hi(u)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// the largest magnitude (drops NaNs)
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 constexpr int MAX_WARPS = 16;
 
@@ -75,22 +111,26 @@ __device__ __forceinline__ int round_exact(float p, float t, float top) {
 
 // Eight values of p as bytes.  Adding 1.5 x 2^23 leaves the rounded integer in a float's low bits, two's
 // complement, so neither the rounding nor the conversion takes the slow conversion unit; quotients within
-// 5e-5 of a half (127 x 2^-22 = 3e-5) are decided again.
-__device__ __forceinline__ uint2 quantise8(const float (&p)[8], float inv, float top) {
+// 5e-5 of a half (127 x 2^-24 = 8e-6) are decided again.
+__device__ __forceinline__ uint2 quantise8(const F2 (&p)[4], float inv, float top) {
   constexpr float MAGIC = 12582912.0f;
+  const F2 inv2 = pack2(inv, inv), magic2 = pack2(MAGIC, MAGIC), minus2 = pack2(-1.0f, -1.0f);
   uint32_t u[8];
   float far = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float t = p[j] * inv, m = t + MAGIC;
-    far = fmaxf(far, fabsf(t - (m - MAGIC)));
-    u[j] = __float_as_uint(m);
+  for (int j = 0; j < 4; ++j) {
+    const F2 m = fma2(p[j], inv2, magic2);
+    const float2 off = unpack2(fma2(p[j], inv2, fma2(m, minus2, magic2)));
+    far = max_abs(far, off.x, off.y);
+    const float2 r = unpack2(m);
+    u[2 * j] = __float_as_uint(r.x), u[2 * j + 1] = __float_as_uint(r.y);
   }
   if (far > 0.49995f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float t = p[j] * inv;
-      if (fabsf(t - (__uint_as_float(u[j]) - MAGIC)) > 0.49995f) u[j] = (uint32_t)round_exact(p[j], t, top);
+      const float2 two = unpack2(p[j >> 1]);
+      const float x = (j & 1) ? two.y : two.x, t = x * inv;
+      if (fabsf(t - (__uint_as_float(u[j]) - MAGIC)) > 0.49994f) u[j] = (uint32_t)round_exact(x, t, top);
     }
   }
   const uint32_t a = __byte_perm(u[0], u[1], 0x0040), b = __byte_perm(u[2], u[3], 0x0040);
@@ -154,48 +194,54 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
     const uint32_t at = base + slot * slot_bytes;
     slot = slot + 1 == DEPTH ? 0 : slot + 1;
     // vector i of h
-    auto load_h = [&](int i, float (&h)[8], bool store) {
+    auto load_h = [&](int i, bool store) {
       const int c = threadIdx.x + i * blockDim.x;
       uint4 h4 = make_uint4(0, 0, 0, 0);
       if (c < vecs) {
         h4 = lds16(at + 16 * c);
         if (RES) {
           const uint4 r4 = lds16(at + row_bytes + 16 * c);
-          auto sum2 = [](uint32_t u, uint32_t r) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(bf_lo(u) + bf_lo(r), bf_hi(u) + bf_hi(r));
-            return *reinterpret_cast<const uint32_t*>(&h2);
-          };
+          auto sum2 = [](uint32_t u, uint32_t r) { return pack_bf(bf_lo(u) + bf_lo(r), bf_hi(u) + bf_hi(r)); };
           h4 = make_uint4(sum2(h4.x, r4.x), sum2(h4.y, r4.y), sum2(h4.z, r4.z), sum2(h4.w, r4.w));
           if (store) __stcs(reinterpret_cast<uint4*>(a.res + row * a.ldr) + c, h4);
         }
       }
-      h[0] = bf_lo(h4.x), h[1] = bf_hi(h4.x), h[2] = bf_lo(h4.y), h[3] = bf_hi(h4.y);
-      h[4] = bf_lo(h4.z), h[5] = bf_hi(h4.z), h[6] = bf_lo(h4.w), h[7] = bf_hi(h4.w);
+      return h4;
     };
-    auto load_w = [&](int i, float (&w)[8]) {
-      w[0] = bf_lo(hw[i].x), w[1] = bf_hi(hw[i].x), w[2] = bf_lo(hw[i].y), w[3] = bf_hi(hw[i].y);
-      w[4] = bf_lo(hw[i].z), w[5] = bf_hi(hw[i].z), w[6] = bf_lo(hw[i].w), w[7] = bf_hi(hw[i].w);
-    };
-    float p[V][8];
+    // p: with a norm as fp32 pairs, else h's bf16 pairs themselves
+    F2 p[V][4];
+    uint4 kept[V];
     float top = 0.0f, sum = NORM ? w_bad : 0.0f;
-    unsigned top_bits = 0;  // without a norm: the largest magnitude's bits, where a NaN is above all
+    unsigned top_bits = 0;  // the largest magnitude's bits (without a norm a NaN is above all)
+    if (NORM) {
+      F2 sum2 = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float h[8], w[8];
-      load_h(i, h, true);
-      load_w(i, w);
+      for (int i = 0; i < V; ++i) {
+        const uint4 h4 = load_h(i, true);
+        const uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, w[4] = {hw[i].x, hw[i].y, hw[i].z, hw[i].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        p[i][j] = NORM ? h[j] * w[j] : h[j];
-        if (NORM) {
-          sum = fmaf(h[j], h[j], sum);
-          top = fmaxf(top, fabsf(p[i][j]));  // (drops a NaN; one in h shows in the sum)
-        } else {
-          top_bits = max(top_bits, __float_as_uint(fabsf(p[i][j])));
+        for (int j = 0; j < 4; ++j) {
+          const F2 h2 = bf2(h[j]);
+          p[i][j] = mul2(h2, bf2(w[j]));
+          sum2 = fma2(h2, h2, sum2);
+          const float2 two = unpack2(p[i][j]);
+          top = max_abs(top, two.x, two.y);  // (drops a NaN; one in h shows in the sum)
         }
       }
+      const float2 two = unpack2(sum2);
+      sum += two.x + two.y;
+      top_bits = __float_as_uint(top);
+    } else {
+      uint32_t top2 = 0;  // bits of bf16 magnitudes, the same order
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        kept[i] = load_h(i, true);
+        constexpr uint32_t ABS = 0x7fff7fffu;
+        top2 = __vimax3_u16x2(top2, kept[i].x & ABS, kept[i].y & ABS);
+        top2 = __vimax3_u16x2(top2, kept[i].z & ABS, kept[i].w & ABS);
+      }
+      top_bits = max(top2 << 16, top2 & 0xffff0000u);
     }
-    if (NORM) top_bits = __float_as_uint(top);
     // (by turns: a warp may be at the next row's before another has read this one's)
     block_reduce(top_bits, sum, s_top[turn], s_sum[turn]);
     top = __uint_as_float(top_bits);
@@ -212,16 +258,21 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
       top_bits = 0, sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float h[8], w[8];
-        load_h(i, h, false);
-        load_w(i, w);
+        const uint4 h4 = load_h(i, false);
+        const uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w}, w[4] = {hw[i].x, hw[i].y, hw[i].z, hw[i].w};
+        uint32_t k[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
+          const float hx = bf_lo(h[j]), hy = bf_hi(h[j]), wx = bf_lo(w[j]), wy = bf_hi(w[j]);
           // (a zero times anything finite stays one, whatever the other's size)
-          p[i][j] = !NORM ? h[j] * up : h[j] == 0.0f || w[j] == 0.0f ? h[j] * w[j] : (h[j] * up) * (w[j] * up);
-          top_bits = max(top_bits, __float_as_uint(fabsf(p[i][j])));
-          sum = fmaf(h[j] * down, h[j] * down, sum);
+          auto scaled = [&](float u, float v) { return u == 0.0f || v == 0.0f ? u * v : (u * up) * (v * up); };
+          const float x = NORM ? scaled(hx, wx) : hx * up, y = NORM ? scaled(hy, wy) : hy * up;
+          p[i][j] = pack2(x, y);
+          k[j] = pack_bf(x, y);  // (exact where it counts, as h is)
+          top_bits = max(top_bits, max(__float_as_uint(fabsf(x)), __float_as_uint(fabsf(y))));
+          sum = fmaf(hx * down, hx * down, fmaf(hy * down, hy * down, sum));
         }
+        kept[i] = make_uint4(k[0], k[1], k[2], k[3]);
       }
       block_reduce(top_bits, sum, s_top[2], s_sum[2]);
       top = __uint_as_float(top_bits);
@@ -242,8 +293,10 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      if (c < vecs)
+      if (c < vecs) {
+        if (!NORM) p[i][0] = bf2(kept[i].x), p[i][1] = bf2(kept[i].y), p[i][2] = bf2(kept[i].z), p[i][3] = bf2(kept[i].w);
         *reinterpret_cast<uint2*>(q + 8 * (long long)c) = inv != 0.0f ? quantise8(p[i], inv, top) : make_uint2(0, 0);
+      }
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
