@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
   const int v0 = (blockIdx.x % STEP_SPLIT) * STEP_ROWS + (threadIdx.x >> 5) * 16;
   const long long b = task / a.heads;
   const int h = (int)(task % a.heads), hk = h / a.share;
+  after_previous();
   const int slot = a.slots[b];
   __nv_bfloat16* o = a.out + b * a.ldo + h * D + v0 + (lane >> 1);
   if (slot < 0 || slot >= a.pool) {
@@ -330,7 +331,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   const uint32_t bars = smem_addr(sm.bars);
   auto bar = [&](int i) { return bars + 8u * i; };
   // which segment, the barriers and the tensor memory, each by a warp, then one barrier
+  // (The first kernel of a call reads nothing before the stream's work before it has ended; the two behind it are
+  // launched when it has passed this, so they wait where they read its results.)
   if (warp == 0) {
+    if (MODE != OUTPUT) asm volatile("griddepcontrol.wait;" ::: "memory");
     Segment s;
     long long number = 0;
     bool found = find_segment(a, p.m, p.segments, blockIdx.x / a.heads, false, &s, &number);
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
-  if (LOCAL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (MODE != OUTPUT) after_previous();
   // A CTA without work: no segment, a padding sequence (its rows zero), a bad slot, an empty sequence (its
   // state stays, or is zeros; the join's where there is one).
   const Segment sg = sm.seg;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     }
     if (warp == COMPUTE_WARPS + 1) tmem_free(tmem, 512);
     // (a kernel behind this one waits for this one alone: it ends after the one before it)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (MODE == OUTPUT) after_previous();
     return;
   }
   float* wsp = p.ws + (number * a.heads + h) * (D * D);
@@ -432,9 +436,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       __syncwarp();
       if (lane == 0) bar_arrive(bar(i));
     };
-    // As a dependent launch all of the above and the first copies overlap the join; the state the segment
-    // starts from is its result.  (By itself the wait is a no-op.)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // All of the above and the first copies overlap the join; the state the segment starts from is its result.
+    if (MODE == OUTPUT) after_previous();
     float S[32];  // S[v = c0 ..][k = r]
     if (resumed) {
       const long long at = (long long)c0 * D + r;
@@ -916,8 +919,6 @@ LaArgs la_args(const void* q, long long ldq, const void* k, long long ldk, const
   return a;
 }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA; }
-
 }  // namespace
 
 extern "C" int kda_la_step(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
@@ -932,13 +933,8 @@ extern "C" int kda_la_step(const void* q, long long ldq, const void* k, long lon
   if (rows > 0x7fffffffLL / STEP_SPLIT / heads) return KDA_EINVAL;
   const LaArgs a = la_args(q, ldq, k, ldk, v, ldv, rows, heads, qk_heads, g, ldg, scale, state_pool, pool_slots,
                            slots, out, ldo);
-  const unsigned grid = (unsigned)(rows * heads * STEP_SPLIT);
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  if (state_dtype == KDA_STATE_BF16)
-    la_step_kernel<true><<<grid, 32 * STEP_WARPS, 0, st>>>(a);
-  else
-    la_step_kernel<false><<<grid, 32 * STEP_WARPS, 0, st>>>(a);
-  return launched();
+  return launch(state_dtype == KDA_STATE_BF16 ? la_step_kernel<true> : la_step_kernel<false>, rows * heads * STEP_SPLIT,
+                32 * STEP_WARPS, 0, 1, static_cast<cudaStream_t>(cuda_stream), a);
 }
 
 namespace {
@@ -991,38 +987,17 @@ bool la_sizes_ok(long long rows, int heads, long long seqs, long long max_len) {
 template <bool BF>
 int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                       const ChunkArgs& p, const Cut& cut, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(cut.segments * p.a.heads), 1, 1);
-  cfg.blockDim = dim3(CHUNK_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = CHUNK_SMEM;
-  cfg.stream = st;
+  const long long grid = cut.segments * p.a.heads;
   // the shared-memory attribute is per device and cheap: set on every call
-  auto big = [](auto* kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) == cudaSuccess;
-  };
-  if (!cut.split) {
-    if (!big(la_chunk_kernel<DIRECT, BF>) ||
-        cudaLaunchKernelEx(&cfg, la_chunk_kernel<DIRECT, BF>, tq, tk, tv, to, p) != cudaSuccess)
+  auto chunks = [&](auto* kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) != cudaSuccess)
       return KDA_ECUDA;
-    return launched();
-  }
-  if (!big(la_chunk_kernel<OWN, false>) || !big(la_chunk_kernel<OUTPUT, false>) ||
-      cudaLaunchKernelEx(&cfg, la_chunk_kernel<OWN, false>, tq, tk, tv, to, p) != cudaSuccess)
-    return KDA_ECUDA;
-  // the two kernels behind it may start while the one before ends, and wait where they read its results
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchConfig_t join = cfg;
-  join.gridDim = dim3((unsigned)(p.a.seqs * p.a.heads * JOIN_PARTS), 1, 1);
-  join.blockDim = dim3(256, 1, 1);
-  join.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&join, la_join_kernel<BF>, p) != cudaSuccess ||
-      cudaLaunchKernelEx(&cfg, la_chunk_kernel<OUTPUT, false>, tq, tk, tv, to, p) != cudaSuccess)
-    return KDA_ECUDA;
-  return launched();
+    return launch(kernel, grid, CHUNK_THREADS, CHUNK_SMEM, 1, st, tq, tk, tv, to, p);
+  };
+  if (!cut.split) return chunks(la_chunk_kernel<DIRECT, BF>);
+  int rc = chunks(la_chunk_kernel<OWN, false>);
+  if (rc == KDA_OK) rc = launch(la_join_kernel<BF>, p.a.seqs * p.a.heads * JOIN_PARTS, 256, 0, 1, st, p);
+  return rc == KDA_OK ? chunks(la_chunk_kernel<OUTPUT, false>) : rc;
 }
 
 }  // namespace

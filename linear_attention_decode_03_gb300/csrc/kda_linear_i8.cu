@@ -142,8 +142,9 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
     sm.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = threadIdx.x; i < a.tn; i += THREADS) sm.sx[i] = m0 + i < a.M ? a.sx[m0 + i] : 0.0f;
   if (warp == 2 * GROUP + 1) tmem_alloc(smem_addr(&sm.tmem), 512);
+  after_previous();
+  for (int i = threadIdx.x; i < a.tn; i += THREADS) sm.sx[i] = m0 + i < a.M ? a.sx[m0 + i] : 0.0f;
   tc_before();
   __syncthreads();
   tc_after();
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, CTAS)
   const int8_t* w0 = w + (n0 + g) * a.K + 16 * t;
   const int8_t* w1 = w0 + 8 * a.K;
   const int8_t* xp = x + g * ldx + 16 * t;
+  after_previous();
   float acc[NT][4] = {};
   for (int c0 = warp; c0 < chunks; c0 += ROWS_WARPS * UNROLL) {
     uint4 wa[UNROLL], wb[UNROLL], xb[UNROLL][NT];
@@ -451,9 +453,8 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, CTAS)
 
 template <int NT, int UNROLL, int CTAS>
 int i8_rows_launch(const void* x, long long ldx, const void* w, const I8Args& a, cudaStream_t st) {
-  i8_rows_kernel<NT, UNROLL, CTAS><<<(unsigned)((a.N + 15) / 16), 32 * ROWS_WARPS, 0, st>>>(
-      static_cast<const int8_t*>(x), ldx, static_cast<const int8_t*>(w), a);
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
+  return launch(i8_rows_kernel<NT, UNROLL, CTAS>, (a.N + 15) / 16, 32 * ROWS_WARPS, 0, 1, st,
+                static_cast<const int8_t*>(x), ldx, static_cast<const int8_t*>(w), a);
 }
 
 // A launch: weight-row halves, tokens a tile, K split.
@@ -471,18 +472,8 @@ int ring_stages(int mh, int tn) {
 }
 
 template <int MH>
-void i8_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, long long ctas, int split, cudaStream_t st) {
-  *cfg = {};
-  cfg->gridDim = dim3((unsigned)ctas, 1, 1);
-  cfg->blockDim = dim3(32 * (2 * (4 * MH + X_WARPS) + 2), 1, 1);
-  cfg->dynamicSmemBytes = I8_SMEM;
-  cfg->stream = st;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = (unsigned)split;
-  attr->val.clusterDim.y = 1;
-  attr->val.clusterDim.z = 1;
-  cfg->attrs = attr;
-  cfg->numAttrs = 1;
+constexpr int i8_threads() {
+  return 32 * (2 * (4 * MH + X_WARPS) + 2);
 }
 
 // Clusters of c CTAs that the device holds at once (a cluster stays within one GPC, so fewer
@@ -492,9 +483,17 @@ int clusters_held(int dev, int c) {
   static std::atomic<int> cache[64][MAX_SPLIT + 1];
   int held = dev < 64 ? cache[dev][c].load(std::memory_order_relaxed) : 0;
   if (held <= 0) {
-    cudaLaunchConfig_t cfg;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c, 1, 1);
+    cfg.blockDim = dim3(i8_threads<MH>(), 1, 1);
+    cfg.dynamicSmemBytes = I8_SMEM;
     cudaLaunchAttribute attr[1];
-    i8_config<MH>(&cfg, attr, c, c, nullptr);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     // the shared-memory attribute is per device
     if (cudaFuncSetAttribute(i8_kernel<MH>, cudaFuncAttributeMaxDynamicSharedMemorySize, I8_SMEM) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&held, i8_kernel<MH>, &cfg) != cudaSuccess)
@@ -565,11 +564,7 @@ int i8_launch(const void* x, long long ldx, const void* w, I8Args a, const I8Pla
   a.bufs = bufs_of(p.tn);
   const long long groups = (a.N + 128 * MH - 1) / (128 * MH) * a.tiles_m;
   if (groups * p.split > 0x7fffffffLL) return KDA_EINVAL;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
-  i8_config<MH>(&cfg, attr, groups * p.split, p.split, st);
-  if (cudaLaunchKernelEx(&cfg, i8_kernel<MH>, tx, tw, a) != cudaSuccess) return KDA_ECUDA;
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
+  return launch(i8_kernel<MH>, groups * p.split, i8_threads<MH>(), I8_SMEM, p.split, st, tx, tw, a);
 }
 
 }  // namespace

@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include "kda_ops.h"
+#include "tc.cuh"
 
 namespace {
 
@@ -40,13 +41,6 @@ struct QuantArgs {
   int cols;
   float eps;
 };
-
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
 
 // Two floats in a register pair, for the instructions that work on two at a time.
 using F2 = unsigned long long;
@@ -141,12 +135,6 @@ __device__ __forceinline__ uint2 quantise8(const F2 (&p)[4], float inv, float to
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-
 template <int V, bool RES, bool NORM, int MAXT>
 __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
   constexpr int DEPTH = depth_of(V);
@@ -156,9 +144,10 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
   for (int i = threadIdx.x; i < 3 * MAX_WARPS; i += blockDim.x)
     s_top[i / MAX_WARPS][i % MAX_WARPS] = 0, s_sum[i / MAX_WARPS][i % MAX_WARPS] = 0.0f;
   __syncthreads();
+  after_previous();
   const int vecs = a.cols >> 3;
   const int row_bytes = a.cols * 2, slot_bytes = row_bytes * (RES ? 2 : 1);
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t base = smem_addr(ring);
   // one copy group a row, empty behind the last
   auto fetch = [&](long long row, int slot) {
     if (row < a.rows) {
@@ -198,9 +187,9 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
       const int c = threadIdx.x + i * blockDim.x;
       uint4 h4 = make_uint4(0, 0, 0, 0);
       if (c < vecs) {
-        h4 = lds16(at + 16 * c);
+        h4 = lds128(at + 16 * c);
         if (RES) {
-          const uint4 r4 = lds16(at + row_bytes + 16 * c);
+          const uint4 r4 = lds128(at + row_bytes + 16 * c);
           auto sum2 = [](uint32_t u, uint32_t r) { return pack_bf(bf_lo(u) + bf_lo(r), bf_hi(u) + bf_hi(r)); };
           h4 = make_uint4(sum2(h4.x, r4.x), sum2(h4.y, r4.y), sum2(h4.z, r4.z), sum2(h4.w, r4.w));
           if (store) __stcs(reinterpret_cast<uint4*>(a.res + row * a.ldr) + c, h4);
@@ -302,25 +291,22 @@ __global__ void __launch_bounds__(MAXT) quant_rows_kernel(const QuantArgs a) {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
 template <int V, bool RES, bool NORM, int MAXT>
 int quant_run(const QuantArgs& a, int threads, cudaStream_t st) {
   auto kernel = quant_rows_kernel<V, RES, NORM, MAXT>;
   const int smem = depth_of(V) * a.cols * 2 * (RES ? 2 : 1);
-  int dev = 0, sms = 0, per_sm = 1;
+  int dev = 0, per_sm = 1;
   if (smem > 46 * 1024 &&  // (48 KB with the static part)
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return KDA_ECUDA;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return KDA_ECUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ECUDA;
+  const int sms = sm_count(dev);
+  if (sms <= 0) return KDA_ECUDA;
   if (a.rows > sms &&
       (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1))
     return KDA_ECUDA;
   const long long resident = (long long)sms * per_sm;
-  kernel<<<(unsigned)(a.rows < resident ? a.rows : resident), threads, smem, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
+  return launch(kernel, a.rows < resident ? a.rows : resident, threads, smem, 1, st, a);
 }
 
 template <int V, int MAXT>
@@ -341,7 +327,7 @@ extern "C" int kda_quant_rows(const void* x, long long rows, long long ldx, long
   if (!x || !q || !scales || ldx < cols || ldx % 8 || ldq < cols || ldq % 8) return KDA_EINVAL;
   if (residual && (ldr < cols || ldr % 8)) return KDA_EINVAL;
   if (norm_weight && !(eps >= 0.0f)) return KDA_EINVAL;
-  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(norm_weight, 16) || !aligned(q, 8) || !aligned(scales, 4))
+  if (!ptr_aligned(x, 16) || !ptr_aligned(residual, 16) || !ptr_aligned(norm_weight, 16) || !ptr_aligned(q, 8) || !ptr_aligned(scales, 4))
     return KDA_EINVAL;
   QuantArgs a;
   a.x = static_cast<const __nv_bfloat16*>(x);

@@ -9,6 +9,8 @@
 
 #include <atomic>
 
+#include "kda_ops.h"
+
 namespace {
 
 constexpr long long TC_WAIT_LIMIT = 2000000000ll;  // SM cycles (~1 s) before a wait gives up
@@ -229,8 +231,39 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, int col, int r
 // this thread's stores have read their shared memory
 __device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
+// Every kernel of these operators is launched so that it may start while the one before it in the stream ends
+// (launch()).  This waits for that one and its writes; the kernel behind may then be set up.  Nothing before it
+// touches global memory.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // host
+
+// A launch whose CTAs may be placed before the stream's work before it has ended: they call after_previous().
+// cluster > 1: that many CTAs a cluster.
+template <class... P, class... A>
+inline int launch(void (*kernel)(P...), long long grid, int threads, int smem, int cluster, cudaStream_t st,
+                  const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return KDA_ECUDA;
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ECUDA;
+}
 
 inline bool ptr_aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 

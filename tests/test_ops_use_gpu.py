@@ -297,6 +297,96 @@ def test_captured_and_replayed():
     assert kda.kda_la_check() == 0 and kda.kda_linear_i8_check() == 0
 
 
+def test_one_after_the_other_without_a_pause(monkeypatch):
+    """Calls whose CTAs may be placed while the call before them ends: prompts, tokens and copies on the same buffers,
+    all queued at once, give what they give with a wait behind every call."""
+    from linear_attention_decode_03_gb300 import ops
+
+    layer = Layer()
+    real = ops._call
+
+    def waiting(name, device, stream, *args):
+        real(name, device, stream, *args)
+        torch.cuda.synchronize()
+
+    rows, turns = (1, 40, 300), 12
+    sources = [[tuple(t.to(DEV) for t in _inputs(n, 80 + i)) for n in rows] for i in range(turns)]
+    long = [_long_call(130), _long_call(131)]
+    slots = torch.tensor([1], dtype=torch.int32, device=DEV)
+    ends = {n: torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in rows}
+    results = []
+    for call in (real, waiting):
+        monkeypatch.setattr(ops, "_call", call)
+        x, res = (torch.zeros(max(rows), HIDDEN, device=DEV).bfloat16() for _ in range(2))
+        state = torch.zeros(2, HEADS, 128, 128, device=DEV)
+        big = torch.empty_like(long[0]["v"])
+        st = long[0]["state"].clone()
+        got = []
+        torch.cuda.synchronize()
+        for i in range(turns):
+            for n, (sx, sr) in zip(rows, sources[i]):
+                x[:n].copy_(sx)
+                res[:n].copy_(sr)
+                y = layer(x[:n], res[:n], state, slots, None if n == 1 else (ends[n], n, slots))
+                x[:n].fill_(float("nan"))
+                got += [y, res[:n].clone()]
+                res[:n].fill_(float("nan"))
+            kda.la_prefill(**{**long[i % 2], "state": st}, out=big)
+            q8, s8 = kda.quant_rows(big.view(-1, 384))
+            big.fill_(float("nan"))
+            got += [q8, s8, st.clone(), state.clone()]
+        torch.cuda.synchronize()
+        results.append(got)
+    for a, b in zip(*results):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+def test_captured_in_branches():
+    """Calls as a graph's first nodes, behind copies, on two branches and where they meet."""
+    layer = Layer()
+    x, res = (t.to(DEV) for t in _inputs(70, 140))
+    src = [t.clone() for t in (x, res)]
+    c = _long_call(141)
+    first = c["state"].clone()
+    tok = {n: c[n][:1] for n in "qkv"}
+    state = torch.zeros(1, 3, 128, 128, device=DEV)
+    slots = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def both(side):
+        main = torch.cuda.current_stream()
+        q0, s0 = kda.quant_rows(src[0], norm_weight=layer.norm)  # nothing before it
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            o1 = kda.la_step(**tok, g=c["g"], state=state, slots=slots)
+            o2 = kda.la_prefill(**c)
+        x.copy_(src[0])
+        res.copy_(src[1])
+        q8, sq = kda.quant_rows(x, residual=res, norm_weight=layer.norm)
+        main.wait_stream(side)
+        y = kda.linear_i8(q8, sq, layer.w_in, layer.s_in)  # behind both
+        z, sz = kda.quant_rows(o2.view(-1, 384))
+        o3 = kda.la_step(**tok, g=c["g"], state=state, slots=slots)
+        return q0, s0, o1, o2, y, z, sz, o3
+
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in both(side)]
+    torch.cuda.synchronize()
+    last, token = c["state"].clone(), state.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = both(side)
+    for _ in range(3):
+        c["state"].copy_(first)
+        state.zero_()
+        x.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        assert torch.equal(c["state"], last) and torch.equal(state, token)
+    assert kda.kda_la_check() == 0 and kda.kda_linear_i8_check() == 0
+
+
 def test_offsets_past_32_bits():
     """A pool of more than 2^31 values, its last slot; rows and weights of more than 2^31 bytes."""
     heads, pool = 96, 1500
