@@ -823,11 +823,13 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
 }
 
 // From the segments' own states to the states they start from, elementwise and in place in
-// the workspace, and to the one behind the last segment, in the pool: four values a thread, JOIN_PARTS CTAs a state, the loads of JOIN_AHEAD segments
-// in flight together.
-constexpr int JOIN_PARTS = 16, JOIN_AHEAD = 8;
+// the workspace, and to the one behind the last segment, in the pool: four values a thread, JOIN_PARTS CTAs a state, the
+// loads of JOIN_AHEAD segments in flight together.  Between the two passes it is all latency: small CTAs, which find
+// room on every SM, 8192 x 1 head 18 -> 16 us for the whole call against 16 of 256 threads; 16 segments ahead and one load
+// a lane for their decays, 8192 x 12 heads 45.5 -> 42.6 against 8 and a load a segment.
+constexpr int JOIN_PARTS = 64, JOIN_AHEAD = 16, JOIN_THREADS = D * D / 4 / JOIN_PARTS;
 template <bool BF>
-__global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
+__global__ void __launch_bounds__(JOIN_THREADS) la_join_kernel(const ChunkArgs p) {
   const LaArgs& a = p.a;
   __shared__ Segment s_seg;
   __shared__ long long s_number;
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long task = blockIdx.x / JOIN_PARTS;
   const long long seq = task / a.heads;
-  const int h = (int)(task % a.heads);
+  const int h = (int)(task % a.heads), lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     Segment s;
     long long number = 0;
@@ -867,17 +869,18 @@ __global__ void __launch_bounds__(256) la_join_kernel(const ChunkArgs p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int s0 = 0; s0 < count; s0 += JOIN_AHEAD, w += JOIN_AHEAD * step, decays += (long long)JOIN_AHEAD * a.heads) {
     float4 own[JOIN_AHEAD];
-    float f[JOIN_AHEAD];
 #pragma unroll
     for (int i = 0; i < JOIN_AHEAD; ++i) {
-      const bool more = s0 + i < count;
-      own[i] = more ? __ldcg(w + i * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-      f[i] = more ? __ldcg(decays + (long long)i * a.heads) : 0.0f;
+      if (s0 + i >= count) break;
+      own[i] = __ldcg(w + i * step);
     }
+    // a segment's decay a lane
+    const float mine = ex2(lane < JOIN_AHEAD && s0 + lane < count ? __ldcg(decays + (long long)lane * a.heads) : 0.0f);
 #pragma unroll
     for (int i = 0; i < JOIN_AHEAD; ++i) {
-      if (s0 + i < count) w[i * step] = S;
-      const float d = ex2(f[i]);  // (1 behind the last)
+      if (s0 + i >= count) break;
+      w[i * step] = S;
+      const float d = __shfl_sync(0xffffffffu, mine, i);
       S = make_float4(fmaf(d, S.x, own[i].x), fmaf(d, S.y, own[i].y), fmaf(d, S.z, own[i].z), fmaf(d, S.w, own[i].w));
     }
   }
@@ -996,7 +999,7 @@ int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   };
   if (!cut.split) return chunks(la_chunk_kernel<DIRECT, BF>);
   int rc = chunks(la_chunk_kernel<OWN, false>);
-  if (rc == KDA_OK) rc = launch(la_join_kernel<BF>, p.a.seqs * p.a.heads * JOIN_PARTS, 256, 0, 1, st, p);
+  if (rc == KDA_OK) rc = launch(la_join_kernel<BF>, p.a.seqs * p.a.heads * JOIN_PARTS, JOIN_THREADS, 0, 1, st, p);
   return rc == KDA_OK ? chunks(la_chunk_kernel<OUTPUT, false>) : rc;
 }
 
