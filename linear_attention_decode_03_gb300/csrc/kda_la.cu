@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 // A long sequence is split into segments to fill the GPU: la_chunk_kernel<OWN> computes each
 // segment's own contribution to the state, la_join_kernel turns these into the states the segments
 // start from and the one behind the last, and la_chunk_kernel<OUTPUT> runs all segments at once for their
-// outputs (its states end as bf16 operands, so hi and mid will do).  Where no sequence needs that,
-// la_chunk_kernel<DIRECT> does all of it in one launch.
+// outputs (its states end as bf16 operands, so hi and mid will do).  la_chunk_kernel<DIRECT> does all of it for a sequence
+// that is not split: for all of them if none is, else in a fourth launch, whose CTAs take the SMs that OUTPUT's leave
+// (16384 tokens and 255 x 64 of 12 heads: 266 us; all in segments 712, none 423).
 constexpr int CHUNK = 128;
 constexpr int BOX = 64 * 128 * 2;          // 64 columns of 128 rows, bf16
 constexpr int TILE = 2 * BOX;              // a 128 x 128 bf16 operand
@@ -226,48 +227,67 @@ __device__ __forceinline__ bool seq_ok(const LaArgs& a, long long begin, long lo
   return begin >= 0 && end >= begin && end <= a.rows && end - begin <= a.max_len;
 }
 
-// Sequences before `seq` have `first` segments together; found by one warp.
 struct Segment {
   int seq, index, count;  // which sequence; which of its `count` segments
   long long begin, end;   // the sequence's rows
 };
-// Segment number `want` of all (by_seq false) or the first segment of sequence `want`
-// (by_seq true), whose number goes to *number.  False if there is none, or if it is not
-// below `limit` with the rest of its sequence: ascending cu_seqlens never get there, and
-// overlapping ones stay within the grid and the workspace.
-__device__ bool find_segment(const LaArgs& a, int m, long long limit, long long want, bool by_seq, Segment* s, long long* number) {
+struct ChunkArgs {
+  LaArgs a;
+  float* ws;        // [parts, heads, 128 (v), 128 (k)]: a segment's own state, then the one it starts from
+  float* decays;    // [parts, heads]: log2 of the decay over a segment
+  int m;            // chunks a segment
+  int least;        // sequences of so many segments are split: 2, 1 (every one), or 0: none is
+  long long parts;  // the split sequences' segments, at most
+};
+// A warp looks for a part, a segment of a split sequence, by its number among all parts (by_seq false), or for the first
+// part of a split sequence, by the sequence's number among its like (by_seq true).  False if there is none, or if the
+// rest of its sequence passes the limit: ascending cu_seqlens never get there, and overlapping ones
+// stay within the workspace.
+__device__ bool find_part(const ChunkArgs& p, long long want, bool by_seq, Segment* s, long long* number) {
+  const LaArgs& a = p.a;
   const int lane = threadIdx.x & 31;
-  long long before = 0;
+  long long before = 0, split_before = 0;
   for (long long i0 = 0; i0 < a.seqs; i0 += 32) {
     const long long i = i0 + lane;
     long long b = 0, e = 0;
     int n = 0;
     if (i < a.seqs) {
       b = a.cu[i], e = a.cu[i + 1];
-      if (seq_ok(a, b, e)) n = (int)seg_count(e - b, m);
+      if (seq_ok(a, b, e)) n = (int)seg_count(e - b, p.m);
+      if (n < p.least) n = 0;
     }
-    long long upto = n;  // segments of the sequences i0 .. i
+    long long upto = n;  // parts of the sequences i0 .. i
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long t = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += t;
     }
-    const bool here = by_seq ? i == want && n > 0 : n > 0 && before + upto - n <= want && want < before + upto;
+    const unsigned split = __ballot_sync(0xffffffffu, n > 0);
+    const long long first = before + upto - n;
+    const bool here = by_seq ? n > 0 && split_before + __popc(split & ((1u << lane) - 1)) == want
+                             : first <= want && want < first + n;
     const unsigned who = __ballot_sync(0xffffffffu, here);
     if (who) {
       const int l = __ffs(who) - 1;
-      const long long first = __shfl_sync(0xffffffffu, before + upto - n, l);
+      const long long f = __shfl_sync(0xffffffffu, first, l);
       s->seq = (int)(i0 + l);
       s->count = __shfl_sync(0xffffffffu, n, l);
       s->begin = __shfl_sync(0xffffffffu, b, l);
       s->end = __shfl_sync(0xffffffffu, e, l);
-      s->index = by_seq ? 0 : (int)(want - first);
-      *number = first + s->index;
-      return first + s->count <= limit;
+      s->index = by_seq ? 0 : (int)(want - f);
+      *number = f + s->index;
+      return f + s->count <= p.parts;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
+    split_before += __popc(split);
   }
   return false;
+}
+// Sequence `seq` by itself, if it is not split.
+__device__ bool find_whole(const ChunkArgs& p, long long seq, Segment* s) {
+  const long long b = p.a.cu[seq], e = p.a.cu[seq + 1];
+  *s = Segment{(int)seq, 0, 1, b, e};
+  return seq_ok(p.a, b, e) && (p.least == 0 || seg_count(e - b, p.m) < p.least);
 }
 
 // the upper 16 bits of two floats, and a float without its lower 16: bf16 parts cut off, not rounded
@@ -281,14 +301,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-
-struct ChunkArgs {
-  LaArgs a;
-  float* ws;      // [segments, heads, 128 (v), 128 (k)]: a segment's own state, then the one it starts from
-  float* decays;  // [segments, heads]: log2 of the decay over a segment
-  int m;          // chunks a segment
-  long long segments;  // at most
-};
 
 enum {  // barriers: completed by copies and MMAs (one arrival), two stages of each, ...
   FULL_Q, FULL_K = FULL_Q + 2, FULL_V = FULL_K + 2, EMPTY_V = FULL_V + 2,
@@ -331,13 +343,15 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   const uint32_t bars = smem_addr(sm.bars);
   auto bar = [&](int i) { return bars + 8u * i; };
   // which segment, the barriers and the tensor memory, each by a warp, then one barrier
-  // (The first kernel of a call reads nothing before the stream's work before it has ended; the two behind it are
-  // launched when it has passed this, so they wait where they read its results.)
+  // The first kernel of a call reads nothing before the stream's work before it has ended; those behind it are
+  // launched when it has passed this, so they wait where they read another's results, or as they end.
+  const bool first = LOCAL || (MODE == DIRECT && p.least == 0);
   if (warp == 0) {
-    if (MODE != OUTPUT) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (first) asm volatile("griddepcontrol.wait;" ::: "memory");
     Segment s;
     long long number = 0;
-    bool found = find_segment(a, p.m, p.segments, blockIdx.x / a.heads, false, &s, &number);
+    const long long task = blockIdx.x / a.heads;
+    const bool found = MODE == DIRECT ? find_whole(p, task, &s) : find_part(p, task, false, &s, &number);
     if (lane == 0) {
       sm.found = found, sm.dead = 0;
       if (found) {
@@ -346,19 +360,21 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         sm.resumed = MODE == OUTPUT || (MODE == DIRECT && a.has_state && a.has_state[s.seq]);
       }
     }
-    if (!LOCAL && blockIdx.x == 0) {  // bad pairs of cu_seqlens are reported once
+    if ((MODE == DIRECT || (MODE == OUTPUT && p.least == 1)) && blockIdx.x == 0) {  // bad pairs of cu_seqlens: once
       bool bad = false;
-      long long all = 0;
+      long long parts = 0;
       for (long long i = lane; i < a.seqs; i += 32) {
         const long long b = a.cu[i], e = a.cu[i + 1];
-        if (seq_ok(a, b, e))
-          all += seg_count(e - b, p.m);
-        else
+        if (!seq_ok(a, b, e)) {
           bad = true;
+        } else if (p.least > 0) {
+          const long long n = seg_count(e - b, p.m);
+          parts += n < p.least ? 0 : n;
+        }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-      if (bad || all > p.segments) atomicOr(&g_la_err, KDA_ERR_SEQ);
+      for (int o = 16; o > 0; o >>= 1) parts += __shfl_xor_sync(0xffffffffu, parts, o);
+      if (bad || parts > p.parts) atomicOr(&g_la_err, KDA_ERR_SEQ);
     }
   } else if (warp == COMPUTE_WARPS) {
     if (lane == 0) {
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
-  if (MODE != OUTPUT) after_previous();
+  if (first) after_previous();
   // A CTA without work: no segment, a padding sequence (its rows zero), a bad slot, an empty sequence (its
   // state stays, or is zeros; the join's where there is one).
   const Segment sg = sm.seg;
@@ -407,7 +423,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
     }
     if (warp == COMPUTE_WARPS + 1) tmem_free(tmem, 512);
     // (a kernel behind this one waits for this one alone: it ends after the one before it)
-    if (MODE == OUTPUT) after_previous();
+    if (!first) after_previous();
     return;
   }
   float* wsp = p.ws + (number * a.heads + h) * (D * D);
@@ -661,6 +677,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         }
       }
     }
+    if (MODE == DIRECT && !first) after_previous();
     if (!LOCAL && lane == 0) tma_store_read();  // before the memory goes
     if (ok && want_last) {
       const long long at = (long long)c0 * D + r;
@@ -836,16 +853,15 @@ __global__ void __launch_bounds__(JOIN_THREADS) la_join_kernel(const ChunkArgs p
   __shared__ int s_found;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long task = blockIdx.x / JOIN_PARTS;
-  const long long seq = task / a.heads;
   const int h = (int)(task % a.heads), lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     Segment s;
     long long number = 0;
-    const bool found = find_segment(a, p.m, p.segments, seq, true, &s, &number);
+    const bool found = find_part(p, task / a.heads, true, &s, &number);
     if (threadIdx.x == 0) s_seg = s, s_number = number, s_found = found;
   }
   __syncthreads();
-  const int slot = a.slots[seq];
+  const int seq = s_found ? s_seg.seq : 0, slot = a.slots[seq];
   if (!s_found || slot < 0 || slot >= a.pool) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -942,43 +958,65 @@ extern "C" int kda_la_step(const void* q, long long ldq, const void* k, long lon
 
 namespace {
 
-// How a prompt call is cut: chunks a segment, and the segments there can be at most.
+// How a prompt call is cut.
 struct Cut {
-  int m;
-  long long segments;
-  bool split;  // some sequence may have several segments
+  int m;                     // chunks a segment
+  int least;                 // ChunkArgs::least
+  long long splits, parts;   // split sequences and their segments, at most
 };
 
-// Time model in us (fitted to 16 shapes, 128 to 16384 rows of 1 to 96 heads, each at 3 to 14 values of m): a chunk
-// and a CTA's start without a split; with one a chunk in both passes, the three kernels' start, another
-// wave, a segment's states through the join.
-constexpr double T_CHUNK = 3.26, T_START = 5.5, T_CHUNK2 = 4.06, T_START2 = 10.0, T_WAVE2 = 5.0, T_JOIN2 = 0.085;
+// Time model in us (fitted to 20 shapes, 37 to 32704 rows of 1 to 96 heads, 1 to 1024 sequences of like and of very unlike
+// lengths, each at up to 14 values of m; its pick takes 1.7 % longer than the best m on average): a chunk and a CTA's
+// start without a split; with one a chunk in both passes, the three kernels' start, another wave, a segment's states through the
+// join, and the launch for the sequences that are not split.
+constexpr double T_CHUNK = 2.97, T_START = 6.7, T_CHUNK2 = 3.96, T_START2 = 8.0, T_WAVE2 = 4.4, T_JOIN2 = 0.072,
+                 T_WHOLE2 = 4.6;
 
 Cut la_cut(long long rows, int heads, long long seqs, long long max_len, int sms) {
-  long long longest = ((max_len < rows ? max_len : rows) + CHUNK - 1) / CHUNK;  // chunks
+  const long long bound = max_len < rows ? max_len : rows;
+  long long longest = (bound + CHUNK - 1) / CHUNK;  // chunks
   if (longest < 1) longest = 1;
-  const double chunks = (double)rows / CHUNK + 0.5 * (double)seqs;
+  const double per_sm = (double)heads / sms;
+  auto waves_of = [&](double tasks) {
+    const double w = tasks * per_sm;
+    return w <= 1.0 ? 1.0 : (double)(long long)(w + 0.999);
+  };
+  // `n` sequences of `tokens` together that are not split, half of a chunk of each empty: a CTA each and head
+  auto whole = [&](double n, double tokens) {
+    return waves_of(n) * ((tokens / CHUNK / n + 0.5) * T_CHUNK + T_START);
+  };
   Cut best = {};
   double least = 1e300;
   for (long long m = 1;; m = m < 8 ? m + 1 : m + m / 8) {
     const bool last = m >= longest;
     if (last) m = longest;
-    const double segs = chunks / (double)m > (double)seqs ? chunks / (double)m : (double)seqs;
-    const double per = chunks / segs;  // chunks of a segment on average
-    const double w = segs * heads / sms;
-    const double waves = w <= 1.0 ? 1.0 : (double)(long long)(w + 0.999);
-    const double run = per * waves > (double)m ? per * waves : (double)m;
-    const double t = last ? run * T_CHUNK + waves * T_START
-                          : run * T_CHUNK2 + T_START2 + (waves - 1.0) * T_WAVE2 + segs * heads * T_JOIN2;
+    double t;
+    if (last) {
+      const double chain = (double)m * T_CHUNK + T_START, all = whole((double)seqs, (double)rows);
+      t = chain > all ? chain : all;
+    } else {
+      // the lengths are not known here: all alike if that makes them longer than a segment, else one of the longest
+      const bool alike = (double)rows > (double)seqs * (double)m * CHUNK;
+      const double n = alike ? (double)seqs : 1.0, tokens = (double)(alike ? rows : bound);
+      const double chunks = tokens / CHUNK + 0.5 * n, segs = tokens / CHUNK / (double)m + 0.5 * n;
+      const double waves = waves_of(segs), per = chunks / segs < (double)m ? chunks / segs : (double)m;
+      t = (per * waves > (double)m ? per * waves : (double)m) * T_CHUNK2 + T_START2 + (waves - 1.0) * T_WAVE2 +
+          segs * heads * T_JOIN2;
+      if (seqs > 1) t += T_WHOLE2;
+      if ((double)seqs > n) t += whole((double)seqs - n, (double)rows - tokens);
+    }
     if (t < least * 0.999) {
       least = t;
       best.m = (int)(m > 0x1000000 ? 0x1000000 : m);
-      best.split = !last;
+      best.least = last ? 0 : seqs > 1 ? 2 : 1;
     }
     if (last) break;
   }
   const long long per = (long long)best.m * CHUNK;
-  best.segments = rows / per + seqs;
+  if (best.least > 0) {  // (with 2 a split sequence is longer than `per`)
+    best.splits = rows / per < seqs ? rows / per : seqs;
+    best.parts = rows / per + best.splits;
+  }
   return best;
 }
 
@@ -990,17 +1028,17 @@ bool la_sizes_ok(long long rows, int heads, long long seqs, long long max_len) {
 template <bool BF>
 int la_prefill_launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                       const ChunkArgs& p, const Cut& cut, cudaStream_t st) {
-  const long long grid = cut.segments * p.a.heads;
   // the shared-memory attribute is per device and cheap: set on every call
-  auto chunks = [&](auto* kernel) {
+  auto chunks = [&](auto* kernel, long long segments) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CHUNK_SMEM) != cudaSuccess)
       return KDA_ECUDA;
-    return launch(kernel, grid, CHUNK_THREADS, CHUNK_SMEM, 1, st, tq, tk, tv, to, p);
+    return launch(kernel, segments * p.a.heads, CHUNK_THREADS, CHUNK_SMEM, 1, st, tq, tk, tv, to, p);
   };
-  if (!cut.split) return chunks(la_chunk_kernel<DIRECT, BF>);
-  int rc = chunks(la_chunk_kernel<OWN, false>);
-  if (rc == KDA_OK) rc = launch(la_join_kernel<BF>, p.a.seqs * p.a.heads * JOIN_PARTS, JOIN_THREADS, 0, 1, st, p);
-  return rc == KDA_OK ? chunks(la_chunk_kernel<OUTPUT, false>) : rc;
+  if (cut.least == 0) return chunks(la_chunk_kernel<DIRECT, BF>, p.a.seqs);
+  int rc = chunks(la_chunk_kernel<OWN, false>, cut.parts);
+  if (rc == KDA_OK) rc = launch(la_join_kernel<BF>, cut.splits * p.a.heads * JOIN_PARTS, JOIN_THREADS, 0, 1, st, p);
+  if (rc == KDA_OK) rc = chunks(la_chunk_kernel<OUTPUT, false>, cut.parts);
+  return rc == KDA_OK && cut.least == 2 ? chunks(la_chunk_kernel<DIRECT, BF>, p.a.seqs) : rc;
 }
 
 }  // namespace
@@ -1012,8 +1050,8 @@ extern "C" long long kda_la_prefill_workspace(long long rows, int heads, long lo
   const int sms = sm_count(dev);
   if (sms <= 0) return 0;
   const Cut cut = la_cut(rows, heads, seqs, max_len, sms);
-  if (!cut.split) return 0;
-  return (cut.segments * heads * (D * D + 1) * 4 + 15) / 16 * 16;
+  if (cut.least == 0) return 0;
+  return (cut.parts * heads * (D * D + 1) * 4 + 15) / 16 * 16;
 }
 
 extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long long ldk, const void* v,
@@ -1028,14 +1066,14 @@ extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long 
                   out, ldo) ||
       !cu_seqlens || !ptr_aligned(cu_seqlens, 4) || !ptr_aligned(has_state, 4))
     return KDA_EINVAL;
-  // the largest grids: a CTA a segment and head, JOIN_PARTS a sequence and head
-  if ((rows / CHUNK + seqs) > 0x7fffffffLL / heads || seqs > 0x7fffffffLL / JOIN_PARTS / heads) return KDA_EINVAL;
+  if ((rows / CHUNK + seqs) > 0x7fffffffLL / heads) return KDA_EINVAL;  // the largest grid: a CTA a segment and head
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ECUDA;
   const int sms = sm_count(dev);
   if (sms <= 0) return KDA_ECUDA;
   const Cut cut = la_cut(rows, heads, seqs, max_len, sms);
-  const long long need = cut.split ? (cut.segments * heads * (D * D + 1) * 4 + 15) / 16 * 16 : 0;
+  if (cut.splits > 0x7fffffffLL / JOIN_PARTS / heads) return KDA_EINVAL;
+  const long long need = cut.least > 0 ? (cut.parts * heads * (D * D + 1) * 4 + 15) / 16 * 16 : 0;
   if (need > 0 && (!workspace || workspace_bytes < need || !ptr_aligned(workspace, 16))) return KDA_EINVAL;
   CUtensorMap tq = {}, tk = {}, tv = {}, to = {};
   if (rows > 0) {
@@ -1052,9 +1090,9 @@ extern "C" int kda_la_prefill(const void* q, long long ldq, const void* k, long 
   p.a = la_args(q, ldq, k, ldk, v, ldv, rows, heads, qk_heads, g, ldg, scale, state_pool, pool_slots, slots, out, ldo);
   p.a.cu = cu_seqlens, p.a.has_state = has_state, p.a.seqs = seqs, p.a.max_len = max_len;
   p.ws = static_cast<float*>(workspace);
-  p.decays = p.ws + cut.segments * heads * (D * D);
+  p.decays = p.ws + cut.parts * heads * (D * D);
   p.m = cut.m;
-  p.segments = cut.segments;
+  p.least = cut.least, p.parts = cut.parts;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   return state_dtype == KDA_STATE_BF16 ? la_prefill_launch<true>(tq, tk, tv, to, p, cut, st)
                                        : la_prefill_launch<false>(tq, tk, tv, to, p, cut, st);

@@ -381,6 +381,55 @@ def test_la_prefill_long(bf16_state):
     _prefill([1030, 1500], 2, 1, 12, False, bf16_state, resume=True)
 
 
+@pytest.mark.parametrize("bf16_state", [False, True])
+@pytest.mark.parametrize("lens", [[40, 0, 1700, 128, 1, 300, 129, 900], [1400, 5], [3, 257, 1400]])
+def test_la_prefill_long_among_short(lens, bf16_state):
+    # some sequences are cut into segments, the others run by themselves in the same call
+    assert kda.la_prefill_workspace(sum(lens) + 3, 2, len(lens), max(lens)) > 0
+    _prefill(lens, 2, 1, 40 + len(lens), True, bf16_state, resume=True, tail=3)
+    _prefill(lens, 2, 2, 50 + len(lens), False, bf16_state, resume=False, tail=3, max_len=4000)
+
+
+@pytest.mark.parametrize("length", [0, 5, 128, 400])
+def test_la_prefill_one_short_sequence_before_many_rows(length):
+    assert kda.la_prefill_workspace(length + 3000, 2, 1, 3000) > 0
+    for resume in (False, True):
+        _prefill([length], 2, 2, 60 + length, True, False, resume, tail=3000, max_len=3000)
+
+
+def test_la_prefill_long_padding_and_bad_values():
+    heads, lens = 2, [1500, 40, 1300, 30, 1400, 20]
+    rows = sum(lens)
+    _, dev, g, r = _attn(rows, heads, heads, 24, False)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    state = _pool(4, heads, False, r).to(DEV)
+
+    def go(cu, slots, max_len=1500):
+        sd = state.clone()
+        out = torch.full((rows, heads, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+        kda.la_prefill(*dev, g.to(DEV), state=sd, slots=torch.tensor(slots, dtype=torch.int32, device=DEV),
+                       cu_seqlens=torch.tensor(cu, dtype=torch.int32, device=DEV), max_len=max_len, out=out,
+                       has_state=torch.ones(6, dtype=torch.int32, device=DEV))
+        return out, sd, kda.kda_la_check()
+
+    assert kda.la_prefill_workspace(rows, heads, 6, 1500) > 0
+    want, sw, flags = go(cu, [0, -1, -1, 1, -1, 2])
+    assert flags == 0 and (want[1500:2840] == 0).all() and torch.equal(sw[3], state[3])
+    out, sd, flags = go(cu, [0, -1, -1, 1, 9, 2])
+    assert flags == kda.KDA_ERR_SLOT
+    assert (out[2870:4270] == 5).all() and torch.equal(sd, sw)
+    out[2870:4270] = 0
+    assert torch.equal(out, want)
+    # the third sequence is longer than max_len allows the first to be; an end before a beginning
+    out, sd, flags = go(cu, [0, -1, -1, 1, -1, 2], 1350)
+    assert flags == kda.KDA_ERR_SEQ and (out[:1500] == 5).all() and torch.equal(sd[[1, 2, 3]], sw[[1, 2, 3]])
+    bad = cu.copy()
+    bad[4] = 2800
+    out, sd, flags = go(bad, [0, -1, -1, 1, -1, 2])
+    assert flags == kda.KDA_ERR_SEQ and torch.equal(out[:1500], want[:1500])
+    assert torch.equal(sd[[0, 2]], sw[[0, 2]]) and torch.equal(sd[[1, 3]], state[[1, 3]])
+
+
 def test_la_prefill_decay_limits():
     # tokens that drop the state, tokens that keep all of it, decays below fp32's range
     lens, heads = [150, 40], 3
