@@ -193,9 +193,10 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 // to tensor memory: 128 columns of scores that become P (64) and lo (64), 128 of hi and
 // mid, 128 of outputs (Q S^T, scaled there by e^{G_i}, PV added on top), 128 of K'^T V.
 //
-// Measured: 8192 tokens x 12 heads 45 us in a replayed graph (segments of 6 chunks; 101 MB, 14.9 us at the
-// copy bandwidth), a chunk 3.3 us in the DIRECT kernel, about 6200 cycles of which 3000 are MMAs; one
-// chunk by itself 8.7 us.
+// Measured: 8192 tokens x 12 heads 43 us in a replayed graph (segments of 6 chunks; 101 MB, 14.9 us at the
+// copy bandwidth): OWN 15 us, the join 7, OUTPUT's chunks 19.  A chunk takes 3.2 us in the DIRECT kernel, about 6200 cycles
+// of which 3950 are MMAs, 1.6 in OWN and 2.9 in OUTPUT; one chunk by itself 7.8 us.  (Keys on eight warps of their own:
+// 5 % less a chunk in DIRECT, no less where 132 CTAs run, and 2 us more for short prompts.)
 //
 // Roles (warps): 0-15 compute, 16 TMA copies (two stages of Q, K, V) and the decays, 17 MMAs.
 //   MMA:     QK QS | mid, hi | lo PV                | QK ...
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(32 * STEP_WARPS) la_step_kernel(const LaArgs a
 // start from and the one behind the last, and la_chunk_kernel<OUTPUT> runs all segments at once for their
 // outputs (its states end as bf16 operands, so hi and mid will do).  la_chunk_kernel<DIRECT> does all of it for a sequence
 // that is not split: for all of them if none is, else in a fourth launch, whose CTAs take the SMs that OUTPUT's leave
-// (16384 tokens and 255 x 64 of 12 heads: 266 us; all in segments 712, none 423).
+// (16384 tokens and 255 x 64 of 12 heads: 256 us; all in segments 712, none 423).
 constexpr int CHUNK = 128;
 constexpr int BOX = 64 * 128 * 2;          // 64 columns of 128 rows, bf16
 constexpr int TILE = 2 * BOX;              // a 128 x 128 bf16 operand
@@ -346,6 +347,10 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   // The first kernel of a call reads nothing before the stream's work before it has ended; those behind it are
   // launched when it has passed this, so they wait where they read another's results, or as they end.
   const bool first = LOCAL || (MODE == DIRECT && p.least == 0);
+  // What ends behind a kernel that it has not waited for: this one does not end before it, for which one CTA's wait will
+  // do where the kernel before takes long (every CTA's would keep the SMs from the others: 8192 tokens of 4 sequences
+  // and 12 heads 50 us).
+  const bool ends_after = !first && (MODE == OUTPUT || blockIdx.x == gridDim.x - 1);
   if (warp == 0) {
     if (first) asm volatile("griddepcontrol.wait;" ::: "memory");
     Segment s;
@@ -396,6 +401,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
   tc_after();
   const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem);
   if (first) after_previous();
+  // (the sequences that are not split need nothing of these kernels: they may start while OUTPUT waits for the join)
+  if (MODE == OUTPUT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // A CTA without work: no segment, a padding sequence (its rows zero), a bad slot, an empty sequence (its
   // state stays, or is zeros; the join's where there is one).
   const Segment sg = sm.seg;
@@ -422,8 +429,8 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
       }
     }
     if (warp == COMPUTE_WARPS + 1) tmem_free(tmem, 512);
-    // (a kernel behind this one waits for this one alone: it ends after the one before it)
-    if (!first) after_previous();
+    // (a kernel behind this one waits for this one alone)
+    if (ends_after) after_previous();
     return;
   }
   float* wsp = p.ws + (number * a.heads + h) * (D * D);
@@ -677,7 +684,7 @@ __global__ void __launch_bounds__(CHUNK_THREADS, 1)
         }
       }
     }
-    if (MODE == DIRECT && !first) after_previous();
+    if (MODE == DIRECT && ends_after) after_previous();
     if (!LOCAL && lane == 0) tma_store_read();  // before the memory goes
     if (ok && want_last) {
       const long long at = (long long)c0 * D + r;
@@ -966,11 +973,11 @@ struct Cut {
 };
 
 // Time model in us (fitted to 20 shapes, 37 to 32704 rows of 1 to 96 heads, 1 to 1024 sequences of like and of very unlike
-// lengths, each at up to 14 values of m; its pick takes 1.7 % longer than the best m on average): a chunk and a CTA's
+// lengths, each at up to 14 values of m; its pick takes 1 % longer than the best m on average): a chunk and a CTA's
 // start without a split; with one a chunk in both passes, the three kernels' start, another wave, a segment's states through the
-// join, and the launch for the sequences that are not split.
-constexpr double T_CHUNK = 2.97, T_START = 6.7, T_CHUNK2 = 3.96, T_START2 = 8.0, T_WAVE2 = 4.4, T_JOIN2 = 0.072,
-                 T_WHOLE2 = 4.6;
+// join, and the launch for the sequences that are not split, which fill the SMs that the parts leave.
+constexpr double T_CHUNK = 3.2, T_START = 6.8, T_CHUNK2 = 4.08, T_START2 = 8.8, T_WAVE2 = 3.8, T_JOIN2 = 0.066,
+                 T_WHOLE2 = 8.5;
 
 Cut la_cut(long long rows, int heads, long long seqs, long long max_len, int sms) {
   const long long bound = max_len < rows ? max_len : rows;
@@ -1000,10 +1007,14 @@ Cut la_cut(long long rows, int heads, long long seqs, long long max_len, int sms
       const double n = alike ? (double)seqs : 1.0, tokens = (double)(alike ? rows : bound);
       const double chunks = tokens / CHUNK + 0.5 * n, segs = tokens / CHUNK / (double)m + 0.5 * n;
       const double waves = waves_of(segs), per = chunks / segs < (double)m ? chunks / segs : (double)m;
-      t = (per * waves > (double)m ? per * waves : (double)m) * T_CHUNK2 + T_START2 + (waves - 1.0) * T_WAVE2 +
-          segs * heads * T_JOIN2;
+      const double run = (per * waves > (double)m ? per * waves : (double)m) * T_CHUNK2;
+      t = run + T_START2 + (waves - 1.0) * T_WAVE2 + segs * heads * T_JOIN2;
       if (seqs > 1) t += T_WHOLE2;
-      if ((double)seqs > n) t += whole((double)seqs - n, (double)rows - tokens);
+      if ((double)seqs > n) {
+        const double left = 1.0 - segs * per_sm;
+        const double rest = whole((double)seqs - n, (double)rows - tokens) - (left > 0.0 ? left : 0.0) * run;
+        if (rest > 0.0) t += rest;
+      }
     }
     if (t < least * 0.999) {
       least = t;

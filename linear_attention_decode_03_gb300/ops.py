@@ -237,7 +237,8 @@ def la_prefill(q, k, v, g, *, state, slots, cu_seqlens, max_len, has_state=None,
     max_len = int(max_len)
     if max_len < 0:
         raise ValueError("max_len must not be negative")
-    need = la_prefill_workspace(rows, heads, seqs, max_len, device=device)
+    # (a chunk of 128 tokens is never cut: the shortest calls need not ask)
+    need = la_prefill_workspace(rows, heads, seqs, max_len, device=device) if max_len > 128 else 0
     if workspace is not None:
         if not (isinstance(workspace, torch.Tensor) and workspace.dtype == torch.uint8 and workspace.device == device
                 and workspace.is_contiguous() and workspace.numel() >= need):
