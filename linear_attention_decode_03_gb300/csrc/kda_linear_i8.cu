@@ -18,7 +18,7 @@
 // the same buffer (store, fence, barriers: 850 cycles) shows, 0.64 against 0.52 us a step.
 //
 // 4111 x 7168 x 6284: 294 us, 1260 TFLOP/s (cuBLAS bf16 here: 1914 in a burst, 1723 sustained), the tensor pipe
-// busy 56 %; 512 rows 45 us; 64 x 1536 x 7168 10.4 us.
+// busy 56 %; 512 rows 45 us; 64 x 1536 x 7168 9.0 us.
 //
 // Roles: two groups of warps widen the even and the odd units of 64 k (one alone took 1000
 // cycles a unit, wait, read, widen and store one after the other), 4 or 8 of them W (a weight row a
@@ -363,8 +363,9 @@ __global__ void __launch_bounds__(32 * (2 * (4 * MH + X_WARPS) + 2), 1)
 // 64-k chunks in turn and add their partial tiles through shared memory, in warp order.  The
 // bound is the weight's bytes; UNROLL chunks of it are in flight a warp, and the CTAS resident
 // CTAs cover each other's latency (loading ahead of the products measured slower, 12.2 against
-// 10.5 us for 1 x 7168 x 6284: the registers cost more CTAs than that hides).  45 MB in 10.5 us, 3 of them the
-// launch; 1 x 7168 x 49376 55.5 us, 6.4 TB/s.
+// 10.5 us for 1 x 7168 x 6284: the registers cost more CTAs than that hides; asynchronous copies into rings of 3 to 8 chunks a
+// warp, with two to four CTAs an SM, 11.3 to 13.1 against 11.6 there, 4.5 to 5.5 against 4.0 for 1 x 1536 x 7168).  45 MB
+// in 11.6 us from a cold L2, 1 x 7168 x 49376 in 57.1: 6.8 TB/s for what lies between, 5 us for start and end.
 constexpr int ROWS_WARPS = 8;
 
 // 16 bytes, zeros where `in` is false; KEEP: in L1 (x, which every CTA of the SM reads).
