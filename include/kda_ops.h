@@ -16,6 +16,8 @@
  * them alive until the call has completed on its stream.  Calls are
  * asynchronous, take no host sync and can be captured into a CUDA graph.  They
  * keep no state between calls, so any host thread may make them.
+ * Kernels may be set up while the stream's work before them still runs (dependent launches); they
+ * touch global memory only when it has ended.
  */
 #ifndef KDA_OPS_H
 #define KDA_OPS_H
